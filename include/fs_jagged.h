@@ -57,7 +57,7 @@ typedef enum {
   FS_ERR_ALIGNMENT = 8    /* host: a pointer is not aligned as documented */
 } fs_status;
 
-typedef enum { FS_F32 = 0, FS_BF16 = 1 } fs_dtype;
+typedef enum { FS_F32 = 0, FS_BF16 = 1, FS_E4M3 = 2 /* fs_rmsnorm's output only */ } fs_dtype;
 typedef enum { FS_SGD = 0, FS_ROWWISE_ADAGRAD = 1 } fs_optim;
 typedef enum {
   FS_PHASE_ALL = 0,
@@ -455,6 +455,109 @@ fs_status fs_emb_sort_rows_sharded(int64_t num_rows, int32_t dim, fs_dtype dtype
                                    const int32_t* pos, int64_t T, const int64_t* shard_offsets, int32_t n,
                                    const uint8_t* is_co, const uint32_t* co_rows, fs_phase phase, int32_t* err,
                                    void* ws, size_t ws_bytes, fs_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Scaled embedding lookup: what the sequence model reads (FreeScale §2.1: an
+ * ID list becomes a sequence of embeddings) in the model's type and scale.
+ *   out[p, :] = scale * table[ids[p], :]   in fp32, rounded once to out_dtype
+ *   table [num_rows, dim] of table_dtype, out [T, dim] of out_dtype (each FS_F32
+ *   or FS_BF16, independently); any dim >= 1.
+ * An ID outside [0, num_rows) sets FS_ERR_ID_RANGE; its output row is zero.
+ * Rows and addresses that allow it (dim a multiple of 8, of 4 where one side
+ * is FS_F32; 16-byte aligned) move in 16-byte accesses, others by element.
+ * ---------------------------------------------------------------------- */
+fs_status fs_emb_lookup_scaled(const void* table, int64_t num_rows, int32_t dim, fs_dtype table_dtype,
+                               const int64_t* ids, int64_t T, float scale, void* out, fs_dtype out_dtype, int32_t* err,
+                               fs_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Gradient of the (scaled) lookup with respect to the table, row by row, by
+ * sorted IDs -- what update_embedding receives in FreeScale Algorithm 2 (lines
+ * 7, 18, 20), for callers that clip, average or apply an optimizer of their own.
+ *   rows      = the distinct IDs, ascending
+ *   row_grads[u, :] = scale * sum over p with ids[p] = rows[u] of dout[p, :]
+ *   count     [1] int64 out: distinct IDs; more than cap_rows sets
+ *             FS_ERR_CAPACITY (the first cap_rows are written, count is the full number)
+ *   ids [T] int64;  dout [T, dim] of dout_dtype;  rows [cap_rows] int64 out;
+ *   row_grads [cap_rows, dim] of grad_dtype out.  Entries past count are left untouched.
+ * Sums are fp32 in an order that follows from the sorted order and T alone
+ * (the same bits run to run), rounded once.  An ID outside [0, num_rows) sets
+ * FS_ERR_ID_RANGE and is left out.  num_rows < 2^32, any dim >= 1.
+ * ---------------------------------------------------------------------- */
+size_t fs_emb_grad_rows_workspace_size(int64_t T, int64_t num_rows, int32_t dim);
+fs_status fs_emb_grad_rows(int64_t num_rows, int32_t dim, const int64_t* ids, int64_t T, const void* dout,
+                           fs_dtype dout_dtype, float scale, int64_t* rows, void* row_grads, fs_dtype grad_dtype,
+                           int64_t cap_rows, int64_t* count, int32_t* err, void* ws, size_t ws_bytes,
+                           fs_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Root-mean-square norm of rows, with the residual's addition in front of it
+ * and, on request, an 8-bit output with a scale per row.
+ *   h = x + res, stored in dtype (sum_out); h = x when res is NULL
+ *   r = 1 / sqrt(mean_d(h_d^2) + eps);   y_d = h_d * r * gamma_d
+ *   y_dtype = dtype: y rounded once.  y_dtype = FS_E4M3: y_scale = max_d |y_d| / 448
+ *   and y = e4m3(y_d / y_scale), to nearest even; a row of zeros has scale 0
+ *   and zeros.  A row with a NaN or an infinity has a NaN scale (or NaN values).
+ * The norm is of h as stored, so the backward pass differentiates what was computed.
+ *   x, res, sum_out [T, dim] of dtype (FS_F32 or FS_BF16); res and sum_out both or
+ *   neither; sum_out may be x or res (in place).  gamma [dim] fp32.  y [T, dim] of y_dtype;
+ *   y_scale [T] fp32, for FS_E4M3 only (NULL otherwise); rstd [T] fp32 = r, or NULL.
+ * 1 <= dim <= 8192, eps >= 0.
+ *
+ * fs_rmsnorm_backward: with n_d = h_d * r and w_d = gamma_d * dy_d
+ *   dh_d = dsum_d + r * (w_d - n_d * mean_e(w_e * n_e))   the gradient of x and of res
+ *   dgamma_d = sum over rows of dy_d * n_d                fp32, [dim], overwritten
+ *   dy, h, dh [T, dim] of dtype (dh may be dy or dsum); h = sum_out (x without a residual), rstd as
+ *   the forward pass left them; dsum [T, dim] of dtype: the gradient that reaches h
+ *   by other ways (the residual stream), or NULL.
+ * An 8-bit output's gradient is that of the unrounded y.  The order of every sum
+ * is fixed: the same bits run to run.  Workspace 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+fs_status fs_rmsnorm(const void* x, const void* res, int64_t T, int32_t dim, fs_dtype dtype, const float* gamma,
+                     float eps, void* sum_out, void* y, fs_dtype y_dtype, float* y_scale, float* rstd,
+                     fs_stream_t stream);
+size_t fs_rmsnorm_backward_workspace_size(int64_t T, int32_t dim);
+fs_status fs_rmsnorm_backward(const void* dy, const void* dsum, const void* h, int64_t T, int32_t dim, fs_dtype dtype,
+                              const float* gamma, const float* rstd, void* dh, float* dgamma, void* ws,
+                              size_t ws_bytes, fs_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention inside each sample of a jagged batch, and its backward pass, which
+ * recomputes the probabilities.  A sample's row is [UIH | candidates] as the
+ * permute leaves it: with L positions, the last cand_len[s] of them candidates,
+ * position i sees key j of its own sample iff
+ *   (j <= i or causal = 0)  and  (j < L - cand_len[s] or j == i)
+ * -- candidates see the history and themselves, never one another.
+ *   x_ij = scale * q_i.k_j;  lse_i = log sum_j exp(x_ij);  out_i = sum_j exp(x_ij - lse_i) v_j
+ *   p_ij = exp(x_ij - lse_i);  ds_ij = p_ij * (dout_i.v_j - dout_i.out_i)
+ *   dq_i = scale * sum_j ds_ij k_j;  dk_j = scale * sum_i ds_ij q_i;  dv_j = sum_i p_ij dout_i
+ * Query head h reads key/value head h * kv_heads / heads; dk and dv sum over the
+ * query heads that share it.  All rows are bf16; products accumulate in fp32, the
+ * softmax is fp32; p and ds enter their products rounded to bf16.
+ *   q [T, heads, head_dim], k, v [T, kv_heads, head_dim]: rows *_stride elements apart
+ *     (slices of one projection's output), 16-byte aligned, strides multiples of 8;
+ *     dq, dk, dv likewise.  out, dout [T, heads, head_dim] contiguous.  lse [heads, T] fp32.
+ *   offsets [S+1] int64 (device), offsets[0] >= 0, non-decreasing, offsets[S] <= T; positions
+ *     of no sample are left untouched in every output.  Bad offsets set
+ *     FS_ERR_BAD_OFFSETS and the sample is skipped.
+ *   cand_len [S] int32 in [0, L], or NULL (no candidates); outside sets
+ *     FS_ERR_INVALID_ARG and is clamped.
+ * Samples never mix (a NaN in one does not reach another); inside a sample a NaN or an
+ * infinity in k or v may reach rows that do not see it.
+ * head_dim 64 or 128; heads a multiple of kv_heads; scale > 0.  Sums have a fixed
+ * order: the same bits run to run.  The workspace (the same query for both passes) holds nothing between calls.
+ * ---------------------------------------------------------------------- */
+size_t fs_jagged_attn_workspace_size(int64_t T, int64_t S, int32_t heads, int32_t kv_heads, int32_t head_dim);
+fs_status fs_jagged_attn(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                         int64_t v_stride, const int64_t* offsets, int64_t S, int64_t T, int32_t heads,
+                         int32_t kv_heads, int32_t head_dim, const int32_t* cand_len, int32_t causal, float scale,
+                         void* out, float* lse, int32_t* err, void* ws, size_t ws_bytes, fs_stream_t stream);
+fs_status fs_jagged_attn_backward(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                  int64_t v_stride, const void* out, const float* lse, const void* dout,
+                                  const int64_t* offsets, int64_t S, int64_t T, int32_t heads, int32_t kv_heads,
+                                  int32_t head_dim, const int32_t* cand_len, int32_t causal, float scale, void* dq,
+                                  int64_t dq_stride, void* dk, int64_t dk_stride, void* dv, int64_t dv_stride,
+                                  int32_t* err, void* ws, size_t ws_bytes, fs_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Utilities.

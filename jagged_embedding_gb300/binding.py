@@ -21,7 +21,7 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libfsjagged.so")
 
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
 SGD, ROWWISE_ADAGRAD = 0, 1
 PHASE_ALL, PHASE_COLLISION, PHASE_EXCLUSIVE, PHASE_COLLISION_THEN_EXCLUSIVE = 0, 1, 2, 3
 
@@ -39,7 +39,9 @@ EXPORTS = [
     "fs_row_bitmap", "fs_collision_split_bitmaps_workspace_size", "fs_collision_split_bitmaps", "fs_emb_gather", "fs_emb_gather_shard_major",
     "fs_emb_backward_adagrad_workspace_size", "fs_emb_backward_adagrad", "fs_emb_sort_rows",
     "fs_emb_gather_sorted", "fs_emb_update_sorted", "fs_emb_sort_rows_sharded_workspace_size",
-    "fs_emb_sort_rows_sharded", "fs_check", "fs_status_string",
+    "fs_emb_sort_rows_sharded", "fs_emb_lookup_scaled", "fs_emb_grad_rows_workspace_size", "fs_emb_grad_rows",
+    "fs_rmsnorm", "fs_rmsnorm_backward_workspace_size", "fs_rmsnorm_backward", "fs_jagged_attn_workspace_size",
+    "fs_jagged_attn", "fs_jagged_attn_backward", "fs_check", "fs_status_string",
     "fs_set_spin_limit", "fs_get_spin_limit", "fs_debug_skip_publish", "fs_launch_count", "fs_version",
 ]
 
@@ -96,6 +98,17 @@ def lib():
                                  C.c_int),
         "fs_emb_backward_adagrad": ([P, P, i64, i32, C.c_int, C.c_int, P, P, i64, P, P, C.c_int, f32, f32, P, P, sz,
                                      P], C.c_int),
+        "fs_emb_lookup_scaled": ([P, i64, i32, C.c_int, P, i64, f32, P, C.c_int, P, P], C.c_int),
+        "fs_emb_grad_rows_workspace_size": ([i64, i64, i32], sz),
+        "fs_emb_grad_rows": ([i64, i32, P, i64, P, C.c_int, f32, P, P, C.c_int, i64, P, P, P, sz, P], C.c_int),
+        "fs_rmsnorm": ([P, P, i64, i32, C.c_int, P, f32, P, P, C.c_int, P, P, P], C.c_int),
+        "fs_rmsnorm_backward_workspace_size": ([i64, i32], sz),
+        "fs_rmsnorm_backward": ([P, P, P, i64, i32, C.c_int, P, P, P, P, P, sz, P], C.c_int),
+        "fs_jagged_attn_workspace_size": ([i64, i64, i32, i32, i32], sz),
+        "fs_jagged_attn": ([P, i64, P, i64, P, i64, P, i64, i64, i32, i32, i32, P, i32, f32, P, P, P, P, sz, P],
+                           C.c_int),
+        "fs_jagged_attn_backward": ([P, i64, P, i64, P, i64, P, P, P, P, i64, i64, i32, i32, i32, P, i32, f32, P, i64,
+                                     P, i64, P, i64, P, P, sz, P], C.c_int),
         "fs_check": ([P, P], C.c_int),
         "fs_status_string": ([C.c_int], C.c_char_p),
         "fs_set_spin_limit": ([i64], None),
@@ -577,3 +590,180 @@ def fs_emb_update_sorted(table, state, grads, T, ws, optim, lr, eps=0.0, phase=P
                                    dtype_code(table), oc, _ptr(grads), int(T), int(phase), float(lr), float(eps),
                                    _ptr(err), _ptr(ws), ws.numel(), _stream(dev)), "fs_emb_update_sorted")
     return err
+
+
+# ------------------------------------------------------------------ sequence block
+
+def _same(t, shape, dtype, name, device):
+    """An output or second operand: exactly this shape and type, contiguous, on the same device."""
+    if t.device != device or tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise FsError(1, f"{name} must be a contiguous {tuple(shape)} tensor of {dtype} on {device}")
+
+
+def fs_emb_lookup_scaled(table, ids, scale=1.0, out=None, out_dtype=None, err=None, T=None):
+    """out[p] = scale * table[ids[p]], computed in fp32 and rounded once to out's type (f32 or bf16)."""
+    _need(ids, torch.int64, "ids")
+    dev = ids.device
+    R, D = _table_shape(table)
+    if table.device != dev:
+        raise FsError(1, "table and ids must be on the same device")
+    T = ids.numel() if T is None else int(T)
+    if T > ids.numel():
+        raise FsError(1, f"ids too small: {ids.numel()} < {T}")
+    if out is None:
+        out = torch.empty(T, D, dtype=table.dtype if out_dtype is None else out_dtype, device=dev)
+    elif out.device != dev or not out.is_contiguous() or out.numel() < T * D:
+        raise FsError(1, "out must be contiguous [>= T, D]")
+    err = new_err(dev) if err is None else err
+    _ok(lib().fs_emb_lookup_scaled(_ptr(table), R, D, dtype_code(table), _ptr(ids), T, float(scale), _ptr(out),
+                                   dtype_code(out), _ptr(err), _stream(dev)), "fs_emb_lookup_scaled")
+    return out, err
+
+
+def emb_grad_rows_workspace_size(T, num_rows, dim):
+    return int(lib().fs_emb_grad_rows_workspace_size(int(T), int(num_rows), int(dim)))
+
+
+def fs_emb_grad_rows(ids, dout, num_rows, scale=1.0, rows=None, row_grads=None, count=None, grad_dtype=torch.float32,
+                     err=None, ws=None):
+    """Gradient of the scaled lookup row by row: the distinct IDs (ascending), their summed dout rows times scale,
+    and their number (on the device).  rows / row_grads are capacity-sized (min(T, num_rows) where allocated here);
+    entries past count are left untouched."""
+    _need(ids, torch.int64, "ids")
+    dev = ids.device
+    T = ids.numel()
+    if dout.dim() != 2 or dout.shape[0] != T or dout.device != dev or not dout.is_contiguous():
+        raise FsError(1, "dout must be a contiguous [T, D] tensor on the device of ids")
+    D = dout.shape[1]
+    cap = min(T, int(num_rows)) if rows is None else rows.numel()
+    rows = torch.empty(cap, dtype=torch.int64, device=dev) if rows is None else rows
+    row_grads = torch.empty(cap, D, dtype=grad_dtype, device=dev) if row_grads is None else row_grads
+    count = torch.empty(1, dtype=torch.int64, device=dev) if count is None else count
+    _need(rows, torch.int64, "rows")
+    _need(count, torch.int64, "count", 1)
+    _same(row_grads, (cap, D), row_grads.dtype, "row_grads", dev)
+    err = new_err(dev) if err is None else err
+    ws = workspace(emb_grad_rows_workspace_size(T, num_rows, D), dev) if ws is None else ws
+    _ok(lib().fs_emb_grad_rows(int(num_rows), D, _ptr(ids), T, _ptr(dout), dtype_code(dout), float(scale), _ptr(rows),
+                               _ptr(row_grads), dtype_code(row_grads), cap, _ptr(count), _ptr(err), _ptr(ws),
+                               ws.numel(), _stream(dev)), "fs_emb_grad_rows")
+    return rows, row_grads, count, err
+
+
+def fs_rmsnorm(x, gamma, eps, res=None, y_dtype=None, sum_out=None, y=None, y_scale=None, rstd=None):
+    """h = x + res; y = h / sqrt(mean(h^2) + eps) * gamma, in x's type or torch.float8_e4m3fn with a scale per row.
+    Returns (y, y_scale, sum_out, rstd); y_scale is None without 8 bits, sum_out is None without a residual."""
+    dev = x.device
+    if x.dim() != 2:
+        raise FsError(1, "x must be [T, D]")
+    T, D = x.shape
+    _need(x, x.dtype, "x")
+    _same(gamma, (D,), torch.float32, "gamma", dev)
+    if res is not None:
+        _same(res, (T, D), x.dtype, "res", dev)
+        sum_out = torch.empty_like(x) if sum_out is None else sum_out
+        _same(sum_out, (T, D), x.dtype, "sum_out", dev)
+    if y is None:
+        y = torch.empty(T, D, dtype=x.dtype if y_dtype is None else y_dtype, device=dev)
+    bits8 = y.dtype == torch.float8_e4m3fn
+    _same(y, (T, D), y.dtype, "y", dev)
+    if bits8:
+        y_scale = torch.empty(T, dtype=torch.float32, device=dev) if y_scale is None else y_scale
+        _same(y_scale, (T,), torch.float32, "y_scale", dev)
+    rstd = torch.empty(T, dtype=torch.float32, device=dev) if rstd is None else rstd
+    _same(rstd, (T,), torch.float32, "rstd", dev)
+    _ok(lib().fs_rmsnorm(_ptr(x), _ptr(res), T, D, dtype_code(x), _ptr(gamma), float(eps), _ptr(sum_out), _ptr(y),
+                         E4M3 if bits8 else dtype_code(y), _ptr(y_scale), _ptr(rstd), _stream(dev)), "fs_rmsnorm")
+    return y, y_scale, sum_out, rstd
+
+
+def rmsnorm_backward_workspace_size(T, dim):
+    return int(lib().fs_rmsnorm_backward_workspace_size(int(T), int(dim)))
+
+
+def fs_rmsnorm_backward(dy, h, gamma, rstd, dsum=None, dh=None, dgamma=None, ws=None):
+    """Gradients (dh, dgamma) of fs_rmsnorm; h and rstd as the forward pass left them, dsum the gradient that
+    reaches h by other ways."""
+    dev = h.device
+    if h.dim() != 2:
+        raise FsError(1, "h must be [T, D]")
+    T, D = h.shape
+    _need(h, h.dtype, "h")
+    _same(dy, (T, D), h.dtype, "dy", dev)
+    _same(gamma, (D,), torch.float32, "gamma", dev)
+    _same(rstd, (T,), torch.float32, "rstd", dev)
+    if dsum is not None:
+        _same(dsum, (T, D), h.dtype, "dsum", dev)
+    dh = torch.empty_like(h) if dh is None else dh
+    dgamma = torch.empty(D, dtype=torch.float32, device=dev) if dgamma is None else dgamma
+    _same(dh, (T, D), h.dtype, "dh", dev)
+    _same(dgamma, (D,), torch.float32, "dgamma", dev)
+    ws = workspace(rmsnorm_backward_workspace_size(T, D), dev) if ws is None else ws
+    _ok(lib().fs_rmsnorm_backward(_ptr(dy), _ptr(dsum), _ptr(h), T, D, dtype_code(h), _ptr(gamma), _ptr(rstd),
+                                  _ptr(dh), _ptr(dgamma), _ptr(ws), ws.numel(), _stream(dev)), "fs_rmsnorm_backward")
+    return dh, dgamma
+
+
+def _rows(t, T, heads, dim, name, device):
+    """[T, heads, dim] bf16 whose rows are contiguous (a slice of a wider row is fine); returns the row stride."""
+    if t.device != device or t.dtype != torch.bfloat16 or tuple(t.shape) != (T, heads, dim):
+        raise FsError(1, f"{name} must be a ({T}, {heads}, {dim}) tensor of torch.bfloat16 on {device}")
+    if (dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim):
+        raise FsError(1, f"{name}: the heads of a position must be contiguous")
+    return t.stride(0) if T > 1 else max(t.stride(0), heads * dim)
+
+
+def jagged_attn_workspace_size(T, S, heads, kv_heads, head_dim):
+    return int(lib().fs_jagged_attn_workspace_size(int(T), int(S), int(heads), int(kv_heads), int(head_dim)))
+
+
+def _attn_shape(q, k, offsets, cand_len):
+    if q.device.type != "cuda" or q.dim() != 3 or k.dim() != 3:
+        raise FsError(1, "q, k, v must be CUDA tensors [T, heads, head_dim]")
+    _need(offsets, torch.int64, "offsets", 1)
+    S = offsets.numel() - 1
+    if cand_len is not None:
+        _need(cand_len, torch.int32, "cand_len", S)
+    return (*q.shape, k.shape[1], S, q.device)
+
+
+def fs_jagged_attn(q, k, v, offsets, scale, causal=True, cand_len=None, out=None, lse=None, err=None, ws=None):
+    """Attention inside each sample of a jagged batch: q [T, H, Dh], k, v [T, Hkv, Dh] (bf16, row-strided), offsets
+    [S + 1]; the last cand_len[s] positions of a sample are candidates that see the history and themselves.
+    Returns (out [T, H, Dh], lse [H, T], err)."""
+    T, H, Dh, Hkv, S, dev = _attn_shape(q, k, offsets, cand_len)
+    qs, ks, vs = (_rows(t, T, h, Dh, n, dev) for t, h, n in ((q, H, "q"), (k, Hkv, "k"), (v, Hkv, "v")))
+    out = torch.empty(T, H, Dh, dtype=torch.bfloat16, device=dev) if out is None else out
+    lse = torch.empty(H, T, dtype=torch.float32, device=dev) if lse is None else lse
+    _same(out, (T, H, Dh), torch.bfloat16, "out", dev)
+    _same(lse, (H, T), torch.float32, "lse", dev)
+    err = new_err(dev) if err is None else err
+    ws = workspace(jagged_attn_workspace_size(T, S, H, Hkv, Dh), dev) if ws is None else ws
+    _ok(lib().fs_jagged_attn(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(offsets), S, T, H, Hkv, Dh, _ptr(cand_len),
+                             int(bool(causal)), float(scale), _ptr(out), _ptr(lse), _ptr(err), _ptr(ws), ws.numel(),
+                             _stream(dev)), "fs_jagged_attn")
+    return out, lse, err
+
+
+def fs_jagged_attn_backward(q, k, v, out, lse, dout, offsets, scale, causal=True, cand_len=None, dq=None, dk=None,
+                            dv=None, err=None, ws=None):
+    """Gradients (dq, dk, dv, err) of fs_jagged_attn, the probabilities recomputed from q, k and lse.  dq, dk, dv
+    may be slices of one [T, H + 2 Hkv, Dh] tensor (allocated so where not given)."""
+    T, H, Dh, Hkv, S, dev = _attn_shape(q, k, offsets, cand_len)
+    qs, ks, vs = (_rows(t, T, h, Dh, n, dev) for t, h, n in ((q, H, "q"), (k, Hkv, "k"), (v, Hkv, "v")))
+    _same(out, (T, H, Dh), torch.bfloat16, "out", dev)
+    _same(dout, (T, H, Dh), torch.bfloat16, "dout", dev)
+    _same(lse, (H, T), torch.float32, "lse", dev)
+    if dq is None and dk is None and dv is None:
+        dq, dk, dv = torch.empty(T, H + 2 * Hkv, Dh, dtype=torch.bfloat16, device=dev).split([H, Hkv, Hkv], dim=1)
+    dq = torch.empty(T, H, Dh, dtype=torch.bfloat16, device=dev) if dq is None else dq
+    dk = torch.empty(T, Hkv, Dh, dtype=torch.bfloat16, device=dev) if dk is None else dk
+    dv = torch.empty(T, Hkv, Dh, dtype=torch.bfloat16, device=dev) if dv is None else dv
+    dqs, dks, dvs = (_rows(t, T, h, Dh, n, dev) for t, h, n in ((dq, H, "dq"), (dk, Hkv, "dk"), (dv, Hkv, "dv")))
+    err = new_err(dev) if err is None else err
+    ws = workspace(jagged_attn_workspace_size(T, S, H, Hkv, Dh), dev) if ws is None else ws
+    _ok(lib().fs_jagged_attn_backward(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(out), _ptr(lse), _ptr(dout),
+                                      _ptr(offsets), S, T, H, Hkv, Dh, _ptr(cand_len), int(bool(causal)), float(scale),
+                                      _ptr(dq), dqs, _ptr(dk), dks, _ptr(dv), dvs, _ptr(err), _ptr(ws), ws.numel(),
+                                      _stream(dev)), "fs_jagged_attn_backward")
+    return dq, dk, dv, err

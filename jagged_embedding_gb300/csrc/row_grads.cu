@@ -1,0 +1,551 @@
+// Gradient of the (scaled) embedding lookup by sorted IDs:
+//   rows = the distinct IDs, ascending;  G[u] = scale * sum over p with ids[p] = rows[u] of dout[p]
+// -- FreeScale (arXiv 2604.24073) Algorithm 2 lines 7, 18 and 20 without the
+// optimizer: what update_embedding receives, for callers that clip, average or
+// apply an optimizer of their own.
+//
+//   1. sort of (row, position): the library's radix passes, or one block in
+//      shared memory for a small batch (one launch instead of a dozen);
+//   2. heads: numbers the distinct rows of the sorted entries (single-pass scan);
+//   3. reduce: a group of lanes per tile of `chunk` sorted entries sums dout
+//      rows in fp32 in entry order; a row inside the tile is written out, a row
+//      that crosses a tile's edge leaves partial sums;
+//   4. join: adds the partial sums of the rows that cross edges, in tile order
+//      (a hot row crosses thousands of tiles: a whole block adds those).
+// The order of every sum follows from the sorted order and T alone: results are
+// the same bits from run to run.
+//
+// Bound by HBM: 8 B of ID and one row of dout per position, one row of G per
+// distinct ID; the sort moves about 20 B per ID and pass beside that.
+#include "convert.cuh"
+#include "fs_common.cuh"
+#include "radix.cuh"
+
+namespace fs {
+namespace {
+
+struct SrcIds {
+  using Key = uint32_t;
+  static constexpr bool kIndexValue = true;  // value = item index
+  static constexpr bool kFetch2 = false;
+  const int64_t* ids;
+  int64_t R;
+  using Raw = int64_t;
+  template <bool>
+  __device__ __forceinline__ Raw fetch(int64_t i) const { return __ldcs(ids + i); }
+  __device__ __forceinline__ bool make(Raw id, int64_t i, int, Key& key, uint32_t& val, int32_t* err) const {
+    if (uint64_t(id) >= uint64_t(R)) {
+      if (err) set_err(err, FS_ERR_ID_RANGE);
+      return false;
+    }
+    key = uint32_t(id);
+    val = uint32_t(i);
+    return true;
+  }
+  __device__ __forceinline__ uint32_t digit(Key key, int shift, int bits, int) const {
+    return (key >> shift) & ((1u << bits) - 1u);
+  }
+};
+
+// ------------------------------------------------------------- numbering the rows
+
+constexpr int kHeadThreads = 256, kHeadItems = 8, kHeadTile = kHeadThreads * kHeadItems;
+
+struct Numbering {
+  int64_t* rows;    // [cap] out
+  int64_t cap;
+  int64_t* count;   // [1] out
+  uint32_t* start;  // [T + 1]: first sorted entry of distinct row u; start[count] = n
+  uint32_t* before; // [tiles]: distinct rows that begin before tile t
+  int chunk_log2;
+};
+
+__global__ void __launch_bounds__(kHeadThreads) heads_kernel(const uint32_t* __restrict__ keys, const int64_t* n_dev,
+                                                             Numbering N, uint64_t* status, uint32_t* ticket,
+                                                             int32_t* err, int64_t limit) {
+  __shared__ uint32_t scan[32];
+  __shared__ int64_t s_tile;
+  __shared__ uint64_t s_excl;
+  if (threadIdx.x == 0) s_tile = atomicAdd(ticket, 1u);  // tiles in the order blocks start: the look-back never waits for a block not yet running
+  __syncthreads();
+  const int64_t n = *n_dev, tile = s_tile;
+  const int64_t ntiles = (n + kHeadTile - 1) / kHeadTile;
+  if (tile >= ntiles) {
+    if (n == 0 && tile == 0 && threadIdx.x == 0) {
+      *N.count = 0;
+      N.start[0] = 0;
+    }
+    return;
+  }
+  const int64_t i0 = tile * kHeadTile + threadIdx.x * kHeadItems;
+  uint32_t k[kHeadItems];
+  uint32_t prev = 0;
+#pragma unroll
+  for (int q = 0; q < kHeadItems; ++q) k[q] = i0 + q < n ? keys[i0 + q] : 0u;
+  if (i0 > 0 && i0 < n) prev = keys[i0 - 1];
+  uint32_t heads = 0, mine = 0;
+#pragma unroll
+  for (int q = 0; q < kHeadItems; ++q) {
+    const bool h = i0 + q < n && (i0 + q == 0 || k[q] != (q ? k[q - 1] : prev));
+    heads |= uint32_t(h) << q;
+    mine += h;
+  }
+  uint32_t total;
+  const uint32_t in_tile = block_exclusive_scan<uint32_t>(mine, scan, &total);
+  if (threadIdx.x < 32) {
+    const uint64_t e = warp_lookback(status, 1, tile, total, err, limit);
+    if (threadIdx.x == 0) s_excl = e;
+  }
+  __syncthreads();
+  uint64_t u = s_excl + in_tile;
+  if (u + mine > uint64_t(n)) return;  // a wait that gave up left no usable number: write nothing
+#pragma unroll
+  for (int q = 0; q < kHeadItems; ++q) {
+    const int64_t i = i0 + q;
+    if (i < n && (i & ((int64_t(1) << N.chunk_log2) - 1)) == 0) N.before[i >> N.chunk_log2] = uint32_t(u);
+    if ((heads >> q) & 1u) {
+      N.start[u] = uint32_t(i);
+      if (int64_t(u) < N.cap) N.rows[u] = int64_t(k[q]);
+      else set_err(err, FS_ERR_CAPACITY);
+      ++u;
+    }
+  }
+  if (tile == ntiles - 1 && threadIdx.x == kHeadThreads - 1) {
+    *N.count = int64_t(u);
+    N.start[u] = uint32_t(n);
+  }
+}
+
+// ------------------------------------------------------------- small batches
+
+// Sort, numbering and the count of a batch of at most 1024 * ITEMS entries by
+// one block: keys in registers, stable counting passes of `bits` (at most 8)
+// bits over shared memory.  An ID out of range takes the key 2^kb - 1 >= R,
+// sorts last and is dropped.
+constexpr int kSmallThreads = 1024, kSmallWarps = kSmallThreads / 32;
+constexpr int64_t kSmallMax = kSmallThreads * 8;
+template <int ITEMS>
+constexpr size_t small_smem() {
+  return (size_t(kSmallThreads) * ITEMS * 2 + kSmallWarps * 256 + 256 + 64) * sizeof(uint32_t);
+}
+
+template <int ITEMS>
+__global__ void __launch_bounds__(kSmallThreads, 1) small_sort_kernel(const int64_t* __restrict__ ids, int32_t T, int64_t R,
+                                                                      int kb, uint32_t* out_k, uint32_t* out_v,
+                                                                      int64_t* n_out, Numbering N, int32_t* err) {
+  extern __shared__ uint32_t sm[];
+  uint32_t* keys = sm;
+  uint32_t* vals = keys + kSmallThreads * ITEMS;
+  uint32_t* hist = vals + kSmallThreads * ITEMS;  // [warps][256]
+  uint32_t* dstart = hist + kSmallWarps * 256;    // [256]
+  uint32_t* red = dstart + 256;                   // [64]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto slot = [&](int i) { return warp * 32 * ITEMS + i * 32 + lane; };  // slot order = item order
+  const uint32_t bad = uint32_t((uint64_t(1) << kb) - 1);
+  uint32_t k[ITEMS], v[ITEMS], rank[ITEMS], valid = 0;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int g = slot(i);
+    k[i] = bad;
+    v[i] = uint32_t(g);
+    if (g < T) {
+      const int64_t id = __ldcs(ids + g);
+      if (uint64_t(id) < uint64_t(R)) {
+        k[i] = uint32_t(id);
+        ++valid;
+      } else {
+        set_err(err, FS_ERR_ID_RANGE);
+      }
+    }
+  }
+  const int passes = (kb + 7) / 8, bits = (kb + passes - 1) / passes, nb = 1 << bits;
+  for (int pass = 0; pass < passes; ++pass) {
+    const int shift = bits * pass;
+    for (int j = threadIdx.x; j < kSmallWarps * nb; j += kSmallThreads) hist[j] = 0u;
+    __syncthreads();
+    uint32_t* wh = hist + warp * nb;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const bool live = slot(i) < T;
+      const uint32_t d = (k[i] >> shift) & uint32_t(nb - 1);
+      const unsigned lv = __ballot_sync(0xffffffffu, live);
+      const unsigned same = __match_any_sync(0xffffffffu, d);
+      const unsigned peers = same & (live ? lv : ~lv);
+      const unsigned lt = __popc(peers & lanemask_lt());
+      const uint32_t base = live ? wh[d] : 0u;
+      rank[i] = base + lt;
+      __syncwarp();
+      if (live && lt == 0) wh[d] = base + __popc(peers);
+      __syncwarp();
+    }
+    __syncthreads();
+    uint32_t tot = 0, x = 0;
+    if (threadIdx.x < 256) {
+      if (int(threadIdx.x) < nb)
+        for (int w = 0; w < kSmallWarps; ++w) {
+          const uint32_t c = hist[w * nb + threadIdx.x];
+          hist[w * nb + threadIdx.x] = tot;
+          tot += c;
+        }
+      x = tot;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) red[warp] = x;
+    }
+    __syncthreads();
+    if (threadIdx.x < 256) {
+      uint32_t b = 0;
+      for (int w = 0; w < warp; ++w) b += red[w];
+      dstart[threadIdx.x] = b + x - tot;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+      if (slot(i) < T) {
+        const uint32_t d = (k[i] >> shift) & uint32_t(nb - 1);
+        const uint32_t at = dstart[d] + hist[warp * nb + d] + rank[i];
+        keys[at] = k[i];
+        vals[at] = v[i];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+      if (slot(i) < T) {
+        k[i] = keys[slot(i)];
+        v[i] = vals[slot(i)];
+      }
+    __syncthreads();
+  }
+  // the sorted entries are in `keys` / `vals`; the valid ones come first
+  uint32_t n, total;
+  block_exclusive_scan<uint32_t>(valid, red, &n);
+  uint32_t mine = 0, heads = 0;
+  // consecutive entries per thread for the numbering
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const uint32_t p = threadIdx.x * ITEMS + i;
+    const bool h = p < n && (p == 0 || keys[p] != keys[p - 1]);
+    heads |= uint32_t(h) << i;
+    mine += h;
+  }
+  uint32_t u = block_exclusive_scan<uint32_t>(mine, red, &total);
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const uint32_t p = threadIdx.x * ITEMS + i;
+    if (p >= n) break;
+    if ((p & ((1u << N.chunk_log2) - 1u)) == 0) N.before[p >> N.chunk_log2] = u;
+    if ((heads >> i) & 1u) {
+      N.start[u] = p;
+      if (int64_t(u) < N.cap) N.rows[u] = int64_t(keys[p]);
+      else set_err(err, FS_ERR_CAPACITY);
+      ++u;
+    }
+    out_k[p] = keys[p];
+    out_v[p] = vals[p];
+  }
+  if (threadIdx.x == 0) {
+    *n_out = n;
+    *N.count = total;
+    N.start[total] = n;
+  }
+}
+
+// ------------------------------------------------------------- reduce
+
+constexpr int kRedThreads = 256, kRedRows = 8;  // dout rows in flight per lane
+
+// LPR lanes (VEC columns each) per tile of 2^chunk_log2 sorted entries;
+// blockIdx.y picks LPR * VEC columns of wider rows.
+template <class EI, class EO, int VEC, int LPR>
+__global__ void __launch_bounds__(kRedThreads) grad_reduce_kernel(
+    const uint32_t* __restrict__ keys, const uint32_t* __restrict__ vals, const int64_t* __restrict__ n_dev,
+    const uint32_t* __restrict__ before, int chunk_log2, const void* __restrict__ dout, int32_t dim, float scale,
+    void* __restrict__ grads, int64_t cap, float* __restrict__ part_head, float* __restrict__ part_tail) {
+  const int64_t n = *n_dev;
+  const int chunk = 1 << chunk_log2;
+  const int64_t t = (int64_t(blockIdx.x) * kRedThreads + threadIdx.x) / LPR;
+  const int64_t s0 = t << chunk_log2;
+  if (s0 >= n) return;
+  const int c = (int(blockIdx.y) * LPR + int(threadIdx.x % LPR)) * VEC;
+  if (c >= dim) return;
+  const int m = n - s0 < chunk ? int(n - s0) : chunk;
+  const uint32_t* tk = keys + s0;
+  const uint32_t* tv = vals + s0;
+  int64_t u = before[t];
+  bool from_prev = s0 > 0 && tk[-1] == tk[0];  // the tile's first row began in an earlier tile
+  if (from_prev) --u;
+  float acc[VEC];
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+  bool open = false;
+  for (int j = 0; j < m; j += kRedRows) {
+    float g[kRedRows][VEC];
+    uint32_t key[kRedRows + 1];
+#pragma unroll
+    for (int q = 0; q < kRedRows; ++q) {
+      if (j + q < m) {
+        key[q] = tk[j + q];
+        load_vec<EI, VEC, true>(dout, int64_t(tv[j + q]) * dim + c, g[q]);
+      }
+    }
+    const bool more = s0 + j + kRedRows < n;
+    key[kRedRows] = more ? tk[j + kRedRows] : 0u;
+#pragma unroll
+    for (int q = 0; q < kRedRows; ++q) {
+      if (j + q < m) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) acc[k] += g[q][k];
+        open = true;
+        if (s0 + j + q + 1 == n || key[q + 1] != key[q]) {  // the row's last entry
+          if (from_prev) {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) part_head[t * dim + c + k] = acc[k];
+          } else if (uint64_t(u) < uint64_t(cap)) {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) acc[k] *= scale;
+            store_vec<EO, VEC, true>(grads, u * dim + c, acc);
+          }
+          from_prev = false;
+          open = false;
+          ++u;
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+        }
+      }
+    }
+  }
+  if (open) {  // the row goes on in the next tile: it began before this one, or here
+    float* part = from_prev ? part_head : part_tail;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) part[t * dim + c + k] = acc[k];
+  }
+}
+
+// One warp per tile in which a row begins that goes on in the next tile:
+// the row's sum is the tile's tail plus the heads of the following tiles up to
+// the row's last.  Rows over more than kLongTiles tiles are added by the whole
+// block: warp w takes every 32nd tile, then the warps' sums in warp order.
+constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32, kLongTiles = 64;
+
+template <class EO>
+__global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const uint32_t* __restrict__ keys,
+                                                                 const int64_t* __restrict__ n_dev,
+                                                                 const uint32_t* __restrict__ start,
+                                                                 const uint32_t* __restrict__ before, int chunk_log2,
+                                                                 int32_t dim, float scale, void* __restrict__ grads,
+                                                                 int64_t cap, const float* __restrict__ part_head,
+                                                                 const float* __restrict__ part_tail) {
+  __shared__ uint32_t long_row[kJoinWarps];
+  __shared__ float sums[kJoinWarps][33];
+  const int64_t n = *n_dev;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t ntiles = (n + (int64_t(1) << chunk_log2) - 1) >> chunk_log2;
+  auto sum_tiles = [&](int64_t t, int64_t first, int64_t last, int64_t step, int c) {
+    float a = 0.f;
+    int64_t v = first;
+    for (; v + 7 * step <= last; v += 8 * step) {
+      float x[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) x[q] = part_head[(v + q * step) * dim + c];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) a += x[q];
+    }
+    for (; v <= last; v += step) a += part_head[v * dim + c];
+    return a;
+  };
+  auto last_tile = [&](uint32_t u) {
+    const int64_t v = int64_t(start[u + 1] - 1) >> chunk_log2;
+    return v < ntiles ? v : ntiles - 1;
+  };
+  auto put = [&](int64_t u, int c, float a) {
+    const float x[1] = {a * scale};
+    store_vec<EO, 1, false>(grads, u * dim + c, x);
+  };
+  for (int64_t t0 = int64_t(blockIdx.x) * kJoinWarps; t0 < ntiles; t0 += int64_t(gridDim.x) * kJoinWarps) {
+    const int64_t t = t0 + warp;
+    bool is_long = false;
+    const int64_t edge = (t + 1) << chunk_log2;
+    if (edge < n && keys[edge - 1] == keys[edge]) {
+      const uint32_t u = before[t + 1] - 1;
+      // (u < n unless the numbering gave up; it begins in this tile)
+      if (int64_t(u) < n && int64_t(u) < cap && int64_t(start[u]) >= (t << chunk_log2)) {
+        const int64_t last = last_tile(u);
+        is_long = last - t > kLongTiles;
+        if (!is_long)
+          for (int c = lane; c < dim; c += 32)
+            put(u, c, part_tail[t * dim + c] + sum_tiles(t, t + 1, last, 1, c));
+      }
+    }
+    if (lane == 0) long_row[warp] = is_long ? 1u : 0u;
+    __syncthreads();
+    for (int w = 0; w < kJoinWarps; ++w) {
+      if (!long_row[w]) continue;  // (the same for every thread)
+      const int64_t tl = t0 + w;
+      const uint32_t u = before[tl + 1] - 1;
+      const int64_t last = last_tile(u);
+      for (int c0 = 0; c0 < dim; c0 += 32) {
+        const int c = c0 + lane;
+        sums[warp][lane] = c < dim ? sum_tiles(tl, tl + 1 + warp, last, kJoinWarps, c) : 0.f;
+        __syncthreads();
+        if (warp == 0 && c < dim) {
+          float a = part_tail[tl * dim + c];
+          for (int q = 0; q < kJoinWarps; ++q) a += sums[q][lane];
+          put(u, c, a);
+        }
+        __syncthreads();
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------- host side
+
+// Entries per reduce tile: 8 for the smallest batches (one step of loads),
+// doubled while more than 32768 tiles remain, at most 128: enough groups of lanes to
+// fill the GPU, few edges (each costs a partial row written and read).
+int chunk_log2_for(int64_t T) {
+  int c = 3;
+  while (c < 7 && (T >> c) > 32768) ++c;
+  return c;
+}
+
+struct GradLayout {
+  radix::SortPlan plan;
+  int chunk_log2 = 3;
+  int64_t tiles = 0, head_tiles = 0;
+};
+
+GradLayout grad_layout(int64_t T, int64_t R) {
+  GradLayout L;
+  L.plan = radix::SortPlan(T, radix::bits_for(uint64_t(R - 1)));
+  L.chunk_log2 = chunk_log2_for(T);
+  L.tiles = (T + (int64_t(1) << L.chunk_log2) - 1) >> L.chunk_log2;
+  L.head_tiles = (T + kHeadTile - 1) / kHeadTile;
+  return L;
+}
+
+struct GradWs {
+  radix::SortWs W;
+  uint32_t *start = nullptr, *before = nullptr;
+  float *part_head = nullptr, *part_tail = nullptr;
+  uint64_t* status = nullptr;  // look-back words of the heads' tiles, then the ticket
+};
+
+template <class Ws>
+void take_grad(const GradLayout& L, int64_t T, int32_t dim, Ws& ws, GradWs& G) {
+  G.start = ws.template take<uint32_t>(size_t(T) + 1);
+  G.before = ws.template take<uint32_t>(size_t(L.tiles) + 1);
+  G.part_head = ws.template take<float>(size_t(L.tiles) * dim);
+  G.part_tail = ws.template take<float>(size_t(L.tiles) * dim);
+  G.status = ws.template take<uint64_t>(size_t(L.head_tiles) + 1);
+}
+
+template <class EI, class EO, int VEC, int LPR>
+void launch_reduce_lpr(const GradLayout& L, const GradWs& G, const uint32_t* sk, const uint32_t* sv, const void* dout,
+                       int32_t dim, float scale, void* grads, int64_t cap, cudaStream_t st) {
+  const int64_t threads = L.tiles * LPR;
+  const dim3 grid(unsigned((threads + kRedThreads - 1) / kRedThreads), unsigned((dim + LPR * VEC - 1) / (LPR * VEC)));
+  grad_reduce_kernel<EI, EO, VEC, LPR><<<grid, kRedThreads, 0, st>>>(sk, sv, G.W.pass.n_valid, G.before, L.chunk_log2,
+                                                                     dout, dim, scale, grads, cap, G.part_head,
+                                                                     G.part_tail);
+}
+
+template <class EI, class EO, int VEC>
+void launch_reduce_vec(const GradLayout& L, const GradWs& G, const uint32_t* sk, const uint32_t* sv, const void* dout,
+                       int32_t dim, float scale, void* grads, int64_t cap, cudaStream_t st) {
+  const int chunks = (dim + VEC - 1) / VEC;
+  if (chunks <= 8) launch_reduce_lpr<EI, EO, VEC, 8>(L, G, sk, sv, dout, dim, scale, grads, cap, st);
+  else if (chunks <= 16) launch_reduce_lpr<EI, EO, VEC, 16>(L, G, sk, sv, dout, dim, scale, grads, cap, st);
+  else launch_reduce_lpr<EI, EO, VEC, 32>(L, G, sk, sv, dout, dim, scale, grads, cap, st);
+}
+
+}  // namespace
+}  // namespace fs
+
+using namespace fs;
+
+extern "C" size_t fs_emb_grad_rows_workspace_size(int64_t T, int64_t num_rows, int32_t dim) {
+  if (T < 0 || T > INT32_MAX || num_rows < 1 || num_rows >= (int64_t(1) << 32) || dim < 1) return 0;
+  const GradLayout L = grad_layout(T, num_rows);
+  WsCounter c;
+  GradWs G;
+  take_grad(L, T, dim, c, G);
+  return c.used + L.plan.bytes() + 256;
+}
+
+extern "C" fs_status fs_emb_grad_rows(int64_t num_rows, int32_t dim, const int64_t* ids, int64_t T, const void* dout,
+                                      fs_dtype dout_dtype, float scale, int64_t* rows, void* row_grads,
+                                      fs_dtype grad_dtype, int64_t cap_rows, int64_t* count, int32_t* err, void* ws,
+                                      size_t ws_bytes, fs_stream_t stream) {
+  FS_NVTX_RANGE();
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (T < 0 || T > INT32_MAX || num_rows < 1 || num_rows >= (int64_t(1) << 32) || dim < 1 || cap_rows < 0 || !count ||
+      !err)
+    return FS_ERR_INVALID_ARG;
+  if ((dout_dtype != FS_F32 && dout_dtype != FS_BF16) || (grad_dtype != FS_F32 && grad_dtype != FS_BF16))
+    return FS_ERR_INVALID_ARG;
+  if (!aligned(count, 8)) return FS_ERR_ALIGNMENT;
+  if (T == 0) return cudaMemsetAsync(count, 0, sizeof(int64_t), st) == cudaSuccess ? FS_OK : FS_ERR_CUDA;
+  if (!ids || !dout || (cap_rows > 0 && (!rows || !row_grads))) return FS_ERR_INVALID_ARG;
+  const size_t ib = dout_dtype == FS_F32 ? 4 : 2, ob = grad_dtype == FS_F32 ? 4 : 2;
+  if (!aligned(ids, 8) || !aligned(rows, 8) || !aligned(dout, ib) || !aligned(row_grads, ob)) return FS_ERR_ALIGNMENT;
+  if (!ws || ws_bytes < fs_emb_grad_rows_workspace_size(T, num_rows, dim)) return FS_ERR_WORKSPACE;
+
+  const GradLayout L = grad_layout(T, num_rows);
+  WsCursor cur(ws, ws_bytes);
+  GradWs G;
+  if (!radix::carve_sort_ws(L.plan, cur, G.W)) return FS_ERR_WORKSPACE;
+  take_grad(L, T, dim, cur, G);
+  if (!cur.ok) return FS_ERR_WORKSPACE;
+  const Numbering N{rows, cap_rows, count, G.start, G.before, L.chunk_log2};
+  int launches = 0;
+  uint32_t *sk = G.W.k[0], *sv = G.W.v[0];
+  if (T <= kSmallMax) {
+    const int kb = radix::bits_for(uint64_t(num_rows));  // room for a key past every row
+    auto small = [&](auto kern, size_t smem) {
+      radix::set_smem(kern, smem);
+      kern<<<1, kSmallThreads, smem, st>>>(ids, int32_t(T), num_rows, kb, sk, sv, G.W.pass.n_valid, N, err);
+    };
+    if (T <= kSmallThreads) small(small_sort_kernel<1>, small_smem<1>());
+    else if (T <= kSmallThreads * 2) small(small_sort_kernel<2>, small_smem<2>());
+    else if (T <= kSmallThreads * 4) small(small_sort_kernel<4>, small_smem<4>());
+    else small(small_sort_kernel<8>, small_smem<8>());
+    launches += 1;
+  } else {
+    const fs_status s = radix::run_sort(SrcIds{ids, num_rows}, L.plan, G.W, err, st, &sk, &sv, &launches);
+    if (s != FS_OK) return s;
+    if (cudaMemsetAsync(G.status, 0, (size_t(L.head_tiles) + 1) * sizeof(uint64_t), st) != cudaSuccess)
+      return FS_ERR_CUDA;
+    heads_kernel<<<unsigned(L.head_tiles), kHeadThreads, 0, st>>>(
+        sk, G.W.pass.n_valid, N, G.status, reinterpret_cast<uint32_t*>(G.status + L.head_tiles), err, spin_limit());
+    launches += 1;
+  }
+  const int vec = ib == 4 ? 4 : 8;
+  // 16-byte loads of dout where rows and addresses allow them (bf16 rows to f32: 4 columns a lane, so that a
+  // lane's f32 store is 16 bytes too); element by element otherwise
+  const bool wide = dim % vec == 0 && aligned(dout, 16) && aligned(row_grads, 16);
+#define FS_GRAD(EI, EO, V)                                                                          \
+  do {                                                                                              \
+    if (wide) launch_reduce_vec<EI, EO, V>(L, G, sk, sv, dout, dim, scale, row_grads, cap_rows, st); \
+    else launch_reduce_vec<EI, EO, 1>(L, G, sk, sv, dout, dim, scale, row_grads, cap_rows, st);      \
+  } while (0)
+  if (ib == 4 && ob == 4) FS_GRAD(F32, F32, 4);
+  else if (ib == 4) FS_GRAD(F32, Bf16, 4);
+  else if (ob == 4) FS_GRAD(Bf16, F32, 4);
+  else FS_GRAD(Bf16, Bf16, 8);
+#undef FS_GRAD
+  const int64_t want = (L.tiles + kJoinWarps - 1) / kJoinWarps, most = int64_t(sm_count()) * 2;
+  const unsigned grid = unsigned(want < most ? want : most);
+  if (ob == 4)
+    grad_join_kernel<F32><<<grid, kJoinThreads, 0, st>>>(sk, G.W.pass.n_valid, G.start, G.before, L.chunk_log2, dim,
+                                                         scale, row_grads, cap_rows, G.part_head, G.part_tail);
+  else
+    grad_join_kernel<Bf16><<<grid, kJoinThreads, 0, st>>>(sk, G.W.pass.n_valid, G.start, G.before, L.chunk_log2, dim,
+                                                          scale, row_grads, cap_rows, G.part_head, G.part_tail);
+  count_launch(launches + 2);
+  return launch_status();
+}
