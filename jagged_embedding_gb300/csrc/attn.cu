@@ -1,178 +1,914 @@
-// Attention inside each sample of a jagged batch, and its backward pass.
-// Row i of a sample of L positions, the last `cand` of them candidates, sees
-// key j iff (j <= i or not causal) and (j < L - cand or j == i).
-//   s = scale * q.k,  lse = log sum_j exp(s_j),  o = sum_j exp(s_j - lse) v_j
-// backward, recomputing p = exp(s - lse):
+// Attention inside each sample of a jagged batch, and its backward pass, on
+// the fifth-generation tensor cores.
+//
+// Row i of a sample of L positions, the last L - uih of them candidates, sees
+// key j iff (j <= i or not causal) and (j < uih or j == i).
+//   x = scale * q.k,  lse = log sum_j exp(x_j),  o = sum_j exp(x_j - lse) v_j
+// backward, recomputing p = exp(x - lse):
 //   delta = do.o,  ds = p * (do.v - delta)
 //   dq = scale * sum_j ds k_j,  dk = scale * sum_i ds q_i,  dv = sum_i p do_i
-#include "convert.cuh"
+//
+// A sample is cut into tiles of 128 positions, the same for queries and keys.
+// A planning kernel lists the tiles of all samples, those with the most work
+// first, so that blocks taken in order leave no long tail.  One block per tile
+// and head then walks the tiles that its rows (or, for dk and dv, its keys)
+// meet: whole tiles that nothing of which is visible are never loaded.
+//
+// The backward pass is two kernels: one block per query tile for dq, one per
+// key tile for dk and dv, each summing in its own accumulators, so every sum
+// has a fixed order and nothing is added atomically; it recomputes x and do.v
+// twice (7 products where a pass with atomic sums of dq needs 5).
+#include <cuda_bf16.h>
+
+#include <mutex>
+
 #include "fs_common.cuh"
+#include "tcgen.cuh"
 
 namespace fs {
 namespace {
 
-struct AttnArgs {
-  const __nv_bfloat16 *q, *k, *v, *out, *dout;
-  int64_t q_stride, k_stride, v_stride;
-  __nv_bfloat16 *o, *dq, *dk, *dv;
-  int64_t dq_stride, dk_stride, dv_stride;
-  const int64_t* offsets;
-  int64_t S, T;
-  int32_t Hq, Hkv;
-  const int32_t* cand;
-  int32_t causal;
-  float scale;
-  float* lse;
-  int32_t* err;
-};
+constexpr int kTile = 128;                   // positions per tile
+constexpr int kBox = kTile * 128;            // bytes of a TMA box: 128 rows of 64 bf16
+constexpr float kLog2e = 1.4426950408889634f;
 
-struct Sample {
-  int64_t begin;
+// ------------------------------------------------------------- planning
+
+struct Tile {
+  int32_t begin;  // first position of the sample
   int32_t L, uih;
+  int32_t t;      // tile index inside the sample
 };
 
-// Sample of position t (binary search; L = 0 where t belongs to none).
-__device__ Sample sample_of(const AttnArgs& a, int64_t t) {
-  int64_t lo = 0, hi = a.S;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (a.offsets[mid + 1] <= t) lo = mid + 1; else hi = mid;
+// Key tiles that query tile t meets: the first n (those of the history up to
+// the causal limit), then, where its rows are all candidates, its own.
+__device__ __forceinline__ int key_tiles(const Tile& x, bool causal, int& own) {
+  const int end = min((x.t + 1) * kTile, x.L);
+  const int lim = causal ? min(x.uih, end) : x.uih;
+  const int n = (lim + kTile - 1) / kTile;
+  own = x.t >= n ? 1 : 0;
+  return n;
+}
+
+// Query tiles that key tile t meets: [first, first + n).
+__device__ __forceinline__ int query_tiles(const Tile& x, bool causal, int& first) {
+  const int all = (x.L + kTile - 1) / kTile;
+  if (x.t * kTile >= x.uih) {  // candidates only: seen by themselves
+    first = x.t;
+    return 1;
   }
-  if (lo >= a.S || a.offsets[lo] > t || a.offsets[lo] < 0 || a.offsets[lo + 1] > a.T) return {0, 0, 0};
-  const int64_t b = a.offsets[lo];
-  const int32_t L = int32_t(a.offsets[lo + 1] - b);
-  int32_t c = a.cand ? a.cand[lo] : 0;
-  c = c < 0 ? 0 : (c > L ? L : c);
-  return {b, L, L - c};
+  first = causal ? x.t : 0;
+  return all - first;
 }
 
-// Offsets and candidate counts are checked once for the whole call.
-__global__ void attn_check_kernel(AttnArgs a) {
-  const int64_t s = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (s >= a.S) return;
-  const int64_t b = a.offsets[s], e = a.offsets[s + 1];
-  if (b < 0 || e < b || e > a.T) {
-    set_err(a.err, FS_ERR_BAD_OFFSETS);
-    return;
-  }
-  const int32_t c = a.cand ? a.cand[s] : 0;
-  if (c < 0 || c > e - b) set_err(a.err, FS_ERR_INVALID_ARG);
-}
+constexpr int kPlanThreads = 1024, kBuckets = 1024;
 
-template <int E>
-__device__ __forceinline__ void row(const __nv_bfloat16* p, int lane, float (&x)[E]) {
-#pragma unroll
-  for (int i = 0; i < E; ++i) x[i] = __bfloat162float(p[lane + 32 * i]);
-}
-
-template <int E>
-__device__ __forceinline__ float dot(const float (&x)[E], const float (&y)[E]) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < E; ++i) s = fmaf(x[i], y[i], s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-
-__device__ __forceinline__ bool sees(const AttnArgs& a, const Sample& s, int i, int j) {
-  return (j <= i || !a.causal) && (j < s.uih || j == i);
-}
-
-// One warp per position and query head; E = head_dim / 32 elements a lane.
-template <int E>
-__global__ void attn_fwd_kernel(AttnArgs a) {
-  const int64_t w = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  const int64_t t = w / a.Hq;
-  const int h = int(w % a.Hq), hk = h * a.Hkv / a.Hq;
-  if (t >= a.T) return;
-  const Sample s = sample_of(a, t);
-  if (s.L == 0) return;
-  const int i = int(t - s.begin);
-  float q[E], o[E] = {}, m = -INFINITY, l = 0.f;
-  row<E>(a.q + t * a.q_stride + h * 32 * E, lane, q);
-  for (int j = 0; j < s.L; ++j) {
-    if (!sees(a, s, i, j)) continue;
-    float k[E], v[E];
-    row<E>(a.k + (s.begin + j) * a.k_stride + hk * 32 * E, lane, k);
-    row<E>(a.v + (s.begin + j) * a.v_stride + hk * 32 * E, lane, v);
-    const float x = dot<E>(q, k) * a.scale, mn = fmaxf(m, x);
-    const float f = expf(m - mn), p = expf(x - mn);
-    l = l * f + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * v[e];
-    m = mn;
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) a.o[(t * a.Hq + h) * 32 * E + lane + 32 * e] = __float2bfloat16_rn(o[e] / l);
-  if (lane == 0) a.lse[int64_t(h) * a.T + t] = m + logf(l);
-}
-
-template <int E>
-__global__ void attn_dq_kernel(AttnArgs a) {
-  const int64_t w = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  const int64_t t = w / a.Hq;
-  const int h = int(w % a.Hq), hk = h * a.Hkv / a.Hq;
-  if (t >= a.T) return;
-  const Sample s = sample_of(a, t);
-  if (s.L == 0) return;
-  const int i = int(t - s.begin);
-  float q[E], o[E], g[E], d[E] = {};
-  row<E>(a.q + t * a.q_stride + h * 32 * E, lane, q);
-  row<E>(a.out + (t * a.Hq + h) * 32 * E, lane, o);
-  row<E>(a.dout + (t * a.Hq + h) * 32 * E, lane, g);
-  const float delta = dot<E>(o, g), lse = a.lse[int64_t(h) * a.T + t];
-  for (int j = 0; j < s.L; ++j) {
-    if (!sees(a, s, i, j)) continue;
-    float k[E], v[E];
-    row<E>(a.k + (s.begin + j) * a.k_stride + hk * 32 * E, lane, k);
-    row<E>(a.v + (s.begin + j) * a.v_stride + hk * 32 * E, lane, v);
-    const float p = expf(dot<E>(q, k) * a.scale - lse);
-    const float ds = p * (dot<E>(g, v) - delta) * a.scale;
-#pragma unroll
-    for (int e = 0; e < E; ++e) d[e] = fmaf(ds, k[e], d[e]);
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) a.dq[t * a.dq_stride + h * 32 * E + lane + 32 * e] = __float2bfloat16_rn(d[e]);
-}
-
-// One warp per position and key/value head, over the query heads that share it.
-template <int E>
-__global__ void attn_dkv_kernel(AttnArgs a) {
-  const int64_t w = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  const int64_t t = w / a.Hkv;
-  const int hk = int(w % a.Hkv), G = a.Hq / a.Hkv;
-  if (t >= a.T) return;
-  const Sample s = sample_of(a, t);
-  if (s.L == 0) return;
-  const int j = int(t - s.begin);
-  float k[E], v[E], dk[E] = {}, dv[E] = {};
-  row<E>(a.k + t * a.k_stride + hk * 32 * E, lane, k);
-  row<E>(a.v + t * a.v_stride + hk * 32 * E, lane, v);
-  for (int h = hk * G; h < (hk + 1) * G; ++h)
-    for (int i = 0; i < s.L; ++i) {
-      if (!sees(a, s, i, j)) continue;
-      const int64_t r = s.begin + i;
-      float q[E], o[E], g[E];
-      row<E>(a.q + r * a.q_stride + h * 32 * E, lane, q);
-      row<E>(a.out + (r * a.Hq + h) * 32 * E, lane, o);
-      row<E>(a.dout + (r * a.Hq + h) * 32 * E, lane, g);
-      const float p = expf(dot<E>(q, k) * a.scale - a.lse[int64_t(h) * a.T + r]);
-      const float ds = p * (dot<E>(g, v) - dot<E>(g, o)) * a.scale;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        dk[e] = fmaf(ds, q[e], dk[e]);
-        dv[e] = fmaf(p, g[e], dv[e]);
+// Lists the tiles of all samples twice, by descending number of key tiles (for
+// queries) and of query tiles (for keys; only where by_key is given): a
+// counting sort over the tile counts by one block.  The order among equals
+// does not matter to any result.
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const int64_t* __restrict__ offsets, int64_t S, int64_t T,
+                                                                 const int32_t* __restrict__ cand, bool causal,
+                                                                 int32_t* ntiles, Tile* by_query, Tile* by_key,
+                                                                 int32_t* err) {
+  __shared__ int32_t hist[2][kBuckets];
+  __shared__ int32_t scan[32];
+  for (int i = threadIdx.x; i < 2 * kBuckets; i += kPlanThreads) (&hist[0][0])[i] = 0;
+  __syncthreads();
+  auto bucket = [](int cost) { return kBuckets - min(cost, kBuckets); };  // most work first
+  auto each = [&](bool report, auto f) {
+    for (int64_t s = threadIdx.x; s < S; s += kPlanThreads) {
+      const int64_t b = offsets[s], e = offsets[s + 1];
+      if (b < 0 || e < b || e > T) {
+        if (report) set_err(err, FS_ERR_BAD_OFFSETS);
+        continue;
+      }
+      const int32_t L = int32_t(e - b);
+      int32_t c = cand ? cand[s] : 0;
+      if (c < 0 || c > L) {
+        if (report) set_err(err, FS_ERR_INVALID_ARG);
+        c = c < 0 ? 0 : L;
+      }
+      Tile x{int32_t(b), L, L - c, 0};
+      for (; x.t * kTile < L; ++x.t) {
+        int own, first;
+        const int nk = key_tiles(x, causal, own) + own;
+        f(x, bucket(nk), bucket(query_tiles(x, causal, first)));
       }
     }
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    a.dk[t * a.dk_stride + hk * 32 * E + lane + 32 * e] = __float2bfloat16_rn(dk[e]);
-    a.dv[t * a.dv_stride + hk * 32 * E + lane + 32 * e] = __float2bfloat16_rn(dv[e]);
+  };
+  // Offsets that are not in order can describe more tiles than the lists hold:
+  // then nothing is listed (the error word says so).
+  int64_t total = 0;
+  each(true, [&](const Tile&, int bq, int bk) {
+    atomicAdd(&hist[0][bq], 1);
+    if (by_key) atomicAdd(&hist[1][bk], 1);
+  });
+  __syncthreads();
+  for (int w = 0; w < (by_key ? 2 : 1); ++w) {
+    int32_t n;
+    const int32_t mine = hist[w][threadIdx.x];
+    const int32_t at = block_exclusive_scan<int32_t>(mine, scan, &n);
+    hist[w][threadIdx.x] = at;
+    total = n;
   }
+  __syncthreads();
+  const int64_t most = T / kTile + (S < T ? S : T);
+  if (total > most) {
+    if (threadIdx.x == 0) {
+      set_err(err, FS_ERR_BAD_OFFSETS);
+      *ntiles = 0;
+    }
+    return;
+  }
+  if (threadIdx.x == 0) *ntiles = int32_t(total);
+  each(false, [&](const Tile& x, int bq, int bk) {
+    by_query[atomicAdd(&hist[0][bq], 1)] = x;
+    if (by_key) by_key[atomicAdd(&hist[1][bk], 1)] = x;
+  });
+}
+
+// ------------------------------------------------------------- shared pieces
+
+struct AttnArgs {
+  const int32_t* ntiles;
+  const Tile* tiles;
+  int32_t heads, kv_heads;
+  int64_t T;
+  bool causal;
+  float scale;
+  __nv_bfloat16* o;        // forward: out
+  const __nv_bfloat16* out;   // backward: out and dout
+  const __nv_bfloat16* dout;
+  float* lse;
+  float* delta;            // [heads, T]: written by the dq kernel, read by the dk / dv kernel
+  __nv_bfloat16 *dq, *dk, *dv;
+  int64_t dq_stride, dk_stride, dv_stride;
+  int32_t* err;
+  uint64_t wait_ns;
+};
+
+// Wait of a whole warp for a barrier's phase, with a limit; sets the error word when it gives up.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t phase, const AttnArgs& a) {
+  if (bulk::warp_wait(bar, phase & 1u, a.wait_ns)) return true;
+  if ((threadIdx.x & 31) == 0) set_err(a.err, FS_ERR_TIMEOUT);
+  return false;
+}
+
+// Tile of `rows` DH columns from position y of head h, as DH / 64 boxes (one thread).
+template <int DH>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int h, int y, uint32_t bar) {
+#pragma unroll
+  for (int b = 0; b < DH / 64; ++b) tc::load_box(dst + b * kBox, map, h * DH + b * 64, y, bar);
+}
+
+// Rows [from, 128) of a loaded tile become zero (whole warp): they belong to
+// another sample or to none, and a NaN there must not meet a zero weight.
+template <int DH>
+__device__ __forceinline__ void zero_rows(unsigned char* tile, int from) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int b = 0; b < DH / 64; ++b) {
+    uint4* p = reinterpret_cast<uint4*>(tile + b * kBox);
+    for (int i = from * 8 + lane; i < kTile * 8; i += 32) p[i] = make_uint4(0, 0, 0, 0);
+  }
+  bulk::fence_async_shared();
+  __syncwarp();
+}
+
+// D[128 x 128] = A B^T over DH columns, both tiles K-major (one thread).
+template <int DH>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b) {
+  constexpr uint32_t id = tc::idesc(kTile, kTile, false);
+#pragma unroll
+  for (int k = 0; k < DH / 16; ++k) {
+    const uint32_t off = (k / 4) * kBox + (k % 4) * 32;
+    tc::mma_ss(d, tc::desc_k(a + off), tc::desc_k(b + off), id, k != 0);
+  }
+}
+
+// D[128 x DH] (+)= A B, A [128 x 128] bf16 in tensor memory, its first 64 columns at a0, the
+// others at a1, B a tile of 128 rows (one thread).
+template <int DH>
+__device__ __forceinline__ void mma_cols(uint32_t d, uint32_t a0, uint32_t a1, uint32_t b, bool acc) {
+  constexpr uint32_t id = tc::idesc(kTile, DH, true);
+#pragma unroll
+  for (int k = 0; k < kTile / 16; ++k)
+    tc::mma_ts(d, (k < 4 ? a0 + 8 * k : a1 + 8 * (k - 4)), tc::desc_mn(b + k * 2048, kBox), id, acc || k != 0);
+}
+
+// 32 fp32 columns, scaled, as bf16 to 64 contiguous bytes.
+__device__ __forceinline__ void store32(__nv_bfloat16* p, const float* x, float f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint4 v;
+    v.x = tc::pack2(x[8 * i] * f, x[8 * i + 1] * f);
+    v.y = tc::pack2(x[8 * i + 2] * f, x[8 * i + 3] * f);
+    v.z = tc::pack2(x[8 * i + 4] * f, x[8 * i + 5] * f);
+    v.w = tc::pack2(x[8 * i + 6] * f, x[8 * i + 7] * f);
+    reinterpret_cast<uint4*>(p)[i] = v;
+  }
+}
+
+template <int DH>
+constexpr int tile_bytes() { return DH / 64 * kBox; }
+
+__device__ __forceinline__ unsigned char* align_smem(unsigned char* p) {
+  return p + ((1024u - (bulk::smem_addr(p) & 1023u)) & 1023u);
+}
+
+// ------------------------------------------------------------- forward
+
+// Four warps hold one query row per thread; the fifth loads tiles and issues
+// the products.  x sits in 128 columns of tensor memory, p (bf16) over it, o
+// beside it: 256 columns, so two blocks share an SM and one block's products
+// run under the other's softmax.
+constexpr int kFwdThreads = 160;
+template <int DH> constexpr int fwd_stages() { return DH == 64 ? 2 : 1; }
+template <int DH> constexpr int fwd_smem() { return tile_bytes<DH>() * (1 + 2 * fwd_stages<DH>()) + 1024; }
+
+template <int DH>
+__global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_constant__ CUtensorMap mq,
+                                                                  const __grid_constant__ CUtensorMap mk,
+                                                                  const __grid_constant__ CUtensorMap mv, AttnArgs a) {
+  constexpr int TB = tile_bytes<DH>(), NS = fwd_stages<DH>();
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) uint64_t bars[10];
+  __shared__ uint32_t tmem_at;
+  const int head = int(blockIdx.x % unsigned(a.heads));
+  const int64_t at = blockIdx.x / unsigned(a.heads);
+  if (at >= *a.ntiles) return;
+  const Tile x = a.tiles[at];
+  const int kv_head = head / (a.heads / a.kv_heads);
+  int own;
+  const int nk = key_tiles(x, a.causal, own);
+  const int n = nk + own;
+  unsigned char* smem = align_smem(raw);
+  const uint32_t q_at = bulk::smem_addr(smem), k_at = q_at + TB, v_at = k_at + NS * TB;
+  const uint32_t bar = bulk::smem_addr(bars);
+  const uint32_t q_full = bar, k_full = bar + 8, v_full = bar + 24, s_full = bar + 40, p_ready = bar + 48, o_done = bar + 56,
+                 drain = bar + 64, fin = bar + 72;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 4) {
+    if (lane == 0) {
+      tc::prefetch_map(&mq), tc::prefetch_map(&mk), tc::prefetch_map(&mv);
+      for (int i = 0; i < 10; ++i) bulk::mbar_init(bar + 8 * i, i == 6 ? 4 : 1);
+      bulk::fence_init();
+    }
+    __syncwarp();
+    tc::alloc(&tmem_at, 256);
+    tc::fence_before();
+  }
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t s_at = tmem_at, o_at = tmem_at + 128;
+  auto key_tile = [&](int j) { return j < nk ? j : x.t; };
+
+  if (warp == 4) {
+    int loaded_k = 0, loaded_v = 0;  // tiles asked for so far
+    auto load_k = [&](int j) {
+      if (lane == 0) {
+        bulk::arrive_expect_tx(k_full + 8 * (j % NS), TB);
+        load_tile<DH>(k_at + (j % NS) * TB, &mk, kv_head, x.begin + key_tile(j) * kTile, k_full + 8 * (j % NS));
+      }
+      loaded_k = j + 1;
+    };
+    auto load_v = [&](int j) {
+      if (lane == 0) {
+        bulk::arrive_expect_tx(v_full + 8 * (j % NS), TB);
+        load_tile<DH>(v_at + (j % NS) * TB, &mv, kv_head, x.begin + key_tile(j) * kTile, v_full + 8 * (j % NS));
+      }
+      loaded_v = j + 1;
+    };
+    if (lane == 0) {
+      bulk::arrive_expect_tx(q_full, TB);
+      load_tile<DH>(q_at, &mq, head, x.begin + x.t * kTile, q_full);
+    }
+    for (int j = 0; j < NS && j < n; ++j) {
+      load_k(j);
+      load_v(j);
+    }
+    bool ok = wait(q_full, 0, a) && wait(k_full, 0, a);
+    if (ok && lane == 0) {
+      mma_rows<DH>(s_at, q_at, k_at);
+      tc::commit(s_full);
+    }
+    for (int j = 0; ok && j < n; ++j) {
+      const int st = j % NS;
+      if (NS == 1 && j + 1 < n) {  // the key tile is free once its product is done
+        if (!(ok = wait(s_full, j, a))) break;
+        load_k(j + 1);
+      }
+      if (!(ok = wait(v_full + 8 * st, j / NS, a))) break;
+      const int valid = x.L - key_tile(j) * kTile;
+      if (valid < kTile) zero_rows<DH>(smem + TB * (1 + NS + st), valid);
+      if (!(ok = wait(p_ready, j, a))) break;
+      tc::fence_after();
+      if (lane == 0) {
+        mma_cols<DH>(o_at, s_at, s_at + 32, v_at + st * TB, j != 0);
+        tc::commit(j + 1 < n ? o_done : fin);
+      }
+      __syncwarp();
+      if (j + 1 < n) {
+        if (!(ok = wait(k_full + 8 * ((j + 1) % NS), (j + 1) / NS, a))) break;
+        if (lane == 0) {
+          // x overwrites p: the products execute in the order they are issued
+          mma_rows<DH>(s_at, q_at, k_at + ((j + 1) % NS) * TB);
+          tc::commit(s_full);
+        }
+        __syncwarp();
+      }
+      if (j + NS < n) {
+        if (NS > 1) load_k(j + NS);  // (p_ready: the product that read this stage is done)
+        if (!(ok = wait(o_done, j, a))) break;
+        load_v(j + NS);
+      }
+    }
+    if (!ok) {  // gave up: let what is in flight land
+      if (lane == 0) tc::commit(drain);
+      bulk::warp_wait(drain, 0, a.wait_ns);
+      bulk::warp_wait(q_full, 0, a.wait_ns);
+      for (int s = 0; s < NS; ++s) {
+        if (loaded_k > s) bulk::warp_wait(k_full + 8 * s, ((loaded_k - 1 - s) / NS) & 1, a.wait_ns);
+        if (loaded_v > s) bulk::warp_wait(v_full + 8 * s, ((loaded_v - 1 - s) / NS) & 1, a.wait_ns);
+      }
+    }
+  } else {
+    const int row = x.t * kTile + threadIdx.x;  // position inside the sample
+    const uint32_t lanes = uint32_t(warp * 32) << 16;
+    const float c = a.scale * kLog2e;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      if (!(ok = wait(s_full, j, a))) break;
+      tc::fence_after();
+      float s[128];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) tc::ld32(s_at + lanes + 32 * b, s + 32 * b);
+      tc::wait_ld();
+#pragma unroll
+      for (int b = 0; b < 4; ++b) tc::tie32(s + 32 * b);
+      const int k0 = key_tile(j) * kTile;
+      if (k0 + kTile > x.uih || (a.causal && k0 + kTile > x.t * kTile)) {
+        const int lim = (a.causal ? min(x.uih, row + 1) : x.uih) - k0, self = row - k0;
+#pragma unroll
+        for (int i = 0; i < 128; ++i) s[i] = (i < lim || i == self) ? s[i] : -INFINITY;
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int i = 4; i < 128; i += 8) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], i + 4 + q < 128 ? fmaxf(s[i + q], s[i + 4 + q]) : s[i + q]);
+      }
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      if (j == 0) {
+        m = top;
+      } else {
+        // the sums keep an older maximum until a row's has grown by 2^8: p stays
+        // below 2^8, its rounding relative, and o is rescaled only then
+        const bool grow = (top - m) * c > 8.f;
+        if (__any_sync(0xffffffffu, grow)) {
+          const float mn = grow ? top : m, f = tc::ex2((m - mn) * c);
+          m = mn;
+          l *= f;
+#pragma unroll
+          for (int b = 0; b < DH / 32; ++b) {
+            float o[32];
+            tc::ld32(o_at + lanes + 32 * b, o);
+            tc::wait_ld();
+            tc::tie32(o);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) tc::mul2(o + i, f, f);
+            tc::st32(o_at + lanes + 32 * b, reinterpret_cast<const uint32_t*>(o));
+          }
+        }
+      }
+      const float mc = -m * c;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      uint32_t p[64];
+#pragma unroll
+      for (int i = 0; i < 128; i += 4) {
+        tc::fma2(s + i, c, c, mc, mc);
+        tc::fma2(s + i + 2, c, c, mc, mc);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s[i + q] = tc::ex2(s[i + q]);
+        tc::add2(sum, s[i], s[i + 1]);
+        tc::add2(sum + 2, s[i + 2], s[i + 3]);
+        p[i / 2] = tc::pack2(s[i], s[i + 1]);
+        p[i / 2 + 1] = tc::pack2(s[i + 2], s[i + 3]);
+        if (i == 60) tc::st32(s_at + lanes, p);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tc::st32(s_at + lanes + 32, p + 32);
+      tc::wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::arrive(p_ready);
+    }
+    if (ok && wait(fin, 0, a)) {
+      tc::fence_after();
+      const int64_t pos = int64_t(x.begin) + row;
+      const float inv = 1.f / l;
+#pragma unroll
+      for (int b = 0; b < DH / 32; ++b) {
+        float o[32];
+        tc::ld32(o_at + lanes + 32 * b, o);
+        tc::wait_ld();
+        tc::tie32(o);
+        if (row < x.L) store32(a.o + (pos * a.heads + head) * DH + 32 * b, o, inv);
+      }
+      if (row < x.L) a.lse[int64_t(head) * a.T + pos] = (m * c + log2f(l)) * (1.f / kLog2e);
+      tc::fence_before();
+    }
+  }
+  __syncthreads();
+  if (warp == 4) {
+    tc::fence_after();
+    tc::dealloc(tmem_at, 256);
+  }
+}
+
+// ------------------------------------------------------------- backward
+
+constexpr int kBwdThreads = 288;  // eight warps for the elementwise part, one for loads and products
+template <int DH> constexpr int bwd_smem() { return tile_bytes<DH>() * 6 + 1024; }
+
+// dq of one query tile and head.  A thread holds one query row and 64 of the
+// 128 keys.  Per key tile: x = q k^T and do v^T into 128 columns each; p = exp(x - lse)
+// stays in registers and frees x, so the next tile's x is computed while
+// ds = p * (do v^T - delta) is formed; ds (bf16) goes over do v^T and multiplies k.
+template <int DH>
+__global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_constant__ CUtensorMap mq,
+                                                                 const __grid_constant__ CUtensorMap mk,
+                                                                 const __grid_constant__ CUtensorMap mv,
+                                                                 const __grid_constant__ CUtensorMap mdo, AttnArgs a) {
+  constexpr int TB = tile_bytes<DH>();
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) uint64_t bars[12];
+  __shared__ uint32_t tmem_at;
+  __shared__ float half_delta[2][kTile];
+  const int head = int(blockIdx.x % unsigned(a.heads));
+  const int64_t at = blockIdx.x / unsigned(a.heads);
+  if (at >= *a.ntiles) return;
+  const Tile x = a.tiles[at];
+  const int kv_head = head / (a.heads / a.kv_heads);
+  int own;
+  const int nk = key_tiles(x, a.causal, own);
+  const int n = nk + own;
+  unsigned char* smem = align_smem(raw);
+  const uint32_t q_at = bulk::smem_addr(smem), do_at = q_at + TB, k_at = do_at + TB, v_at = k_at + 2 * TB;
+  const uint32_t bar = bulk::smem_addr(bars);
+  const uint32_t q_full = bar, k_full = bar + 8, v_full = bar + 24, s_full = bar + 40, dp_full = bar + 48,
+                 s_read = bar + 56, ds_ready = bar + 64, dq_done = bar + 72, drain = bar + 80, fin = bar + 88;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 8) {
+    if (lane == 0) {
+      tc::prefetch_map(&mq), tc::prefetch_map(&mk), tc::prefetch_map(&mv), tc::prefetch_map(&mdo);
+      for (int i = 0; i < 12; ++i) bulk::mbar_init(bar + 8 * i, i == 7 || i == 8 ? 8 : 1);
+      bulk::fence_init();
+    }
+    __syncwarp();
+    tc::alloc(&tmem_at, 512);
+    tc::fence_before();
+  }
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t s_at = tmem_at, dp_at = tmem_at + 128, dq_at = tmem_at + 256;
+  auto key_tile = [&](int j) { return j < nk ? j : x.t; };
+
+  if (warp == 8) {
+    int loaded_k = 0, loaded_v = 0;
+    auto load_k = [&](int j) {
+      if (lane == 0) {
+        bulk::arrive_expect_tx(k_full + 8 * (j & 1), TB);
+        load_tile<DH>(k_at + (j & 1) * TB, &mk, kv_head, x.begin + key_tile(j) * kTile, k_full + 8 * (j & 1));
+      }
+      loaded_k = j + 1;
+    };
+    auto load_v = [&](int j) {
+      if (lane == 0) {
+        bulk::arrive_expect_tx(v_full + 8 * (j & 1), TB);
+        load_tile<DH>(v_at + (j & 1) * TB, &mv, kv_head, x.begin + key_tile(j) * kTile, v_full + 8 * (j & 1));
+      }
+      loaded_v = j + 1;
+    };
+    auto key_ready = [&](int j) {
+      if (!wait(k_full + 8 * (j & 1), j >> 1, a)) return false;
+      const int valid = x.L - key_tile(j) * kTile;
+      if (valid < kTile) zero_rows<DH>(smem + TB * (2 + (j & 1)), valid);
+      return true;
+    };
+    if (lane == 0) {
+      bulk::arrive_expect_tx(q_full, 2 * TB);
+      load_tile<DH>(q_at, &mq, head, x.begin + x.t * kTile, q_full);
+      load_tile<DH>(do_at, &mdo, head, x.begin + x.t * kTile, q_full);
+    }
+    for (int j = 0; j < 2 && j < n; ++j) {
+      load_k(j);
+      load_v(j);
+    }
+    bool ok = wait(q_full, 0, a) && key_ready(0) && wait(v_full, 0, a);
+    if (ok && lane == 0) {
+      mma_rows<DH>(s_at, q_at, k_at);
+      tc::commit(s_full);
+      mma_rows<DH>(dp_at, do_at, v_at);
+      tc::commit(dp_full);
+    }
+    __syncwarp();
+    for (int j = 0; ok && j < n; ++j) {
+      const int st = j & 1, nx = st ^ 1;
+      if (j + 1 < n) {
+        if (!(ok = key_ready(j + 1) && wait(s_read, j, a))) break;
+        tc::fence_after();
+        if (lane == 0) {
+          mma_rows<DH>(s_at, q_at, k_at + nx * TB);
+          tc::commit(s_full);
+        }
+        __syncwarp();
+      }
+      if (!(ok = wait(ds_ready, j, a))) break;
+      tc::fence_after();
+      if (lane == 0) {
+        mma_cols<DH>(dq_at, dp_at, dp_at + 64, k_at + st * TB, j != 0);
+        tc::commit(j + 1 < n ? dq_done : fin);
+      }
+      __syncwarp();
+      if (j + 1 < n) {
+        if (!(ok = wait(v_full + 8 * nx, (j + 1) >> 1, a))) break;
+        if (lane == 0) {
+          // do v^T overwrites ds: the products execute in the order they are issued
+          mma_rows<DH>(dp_at, do_at, v_at + nx * TB);
+          tc::commit(dp_full);
+        }
+        __syncwarp();
+      }
+      if (j + 2 < n) {
+        load_v(j + 2);  // (ds_ready: the product that read this stage is done)
+        if (!(ok = wait(dq_done, j, a))) break;
+        load_k(j + 2);
+      }
+    }
+    if (!ok) {
+      if (lane == 0) tc::commit(drain);
+      bulk::warp_wait(drain, 0, a.wait_ns);
+      bulk::warp_wait(q_full, 0, a.wait_ns);
+      for (int s = 0; s < 2; ++s) {
+        if (loaded_k > s) bulk::warp_wait(k_full + 8 * s, ((loaded_k - 1 - s) >> 1) & 1, a.wait_ns);
+        if (loaded_v > s) bulk::warp_wait(v_full + 8 * s, ((loaded_v - 1 - s) >> 1) & 1, a.wait_ns);
+      }
+    }
+  } else {
+    const int r = threadIdx.x & 127, half = threadIdx.x >> 7;
+    const int row = x.t * kTile + r;
+    const bool live = row < x.L;
+    const int64_t pos = int64_t(x.begin) + row;
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t cols = 64 * half;
+    const float c = a.scale * kLog2e;
+    // delta = dout.out of the row, half of the columns each
+    float d = 0.f;
+    if (live) {
+      const uint4* po = reinterpret_cast<const uint4*>(a.out + (pos * a.heads + head) * DH + half * (DH / 2));
+      const uint4* pg = reinterpret_cast<const uint4*>(a.dout + (pos * a.heads + head) * DH + half * (DH / 2));
+#pragma unroll
+      for (int i = 0; i < DH / 16; ++i) {
+        const uint4 u = __ldg(po + i), w = __ldg(pg + i);
+        const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          d = fmaf(__uint_as_float(uu[q] << 16), __uint_as_float(ww[q] << 16), d);
+          d = fmaf(__uint_as_float(uu[q] & 0xFFFF0000u), __uint_as_float(ww[q] & 0xFFFF0000u), d);
+        }
+      }
+    }
+    half_delta[half][r] = d;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    const float delta = half_delta[0][r] + half_delta[1][r];
+    if (live && half == 0) a.delta[int64_t(head) * a.T + pos] = delta;
+    const float lse2 = live ? a.lse[int64_t(head) * a.T + pos] * kLog2e : 0.f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      if (!(ok = wait(s_full, j, a))) break;
+      tc::fence_after();
+      float p[64];
+      tc::ld32(s_at + lanes + cols, p);
+      tc::ld32(s_at + lanes + cols + 32, p + 32);
+      tc::wait_ld();
+      tc::tie32(p);
+      tc::tie32(p + 32);
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::arrive(s_read);
+      const int k0 = key_tile(j) * kTile + int(cols);
+      const bool masked = k0 - int(cols) + kTile > x.uih || (a.causal && k0 - int(cols) + kTile > x.t * kTile);
+      const int lim = (a.causal ? min(x.uih, row + 1) : x.uih) - k0, self = row - k0;
+#pragma unroll
+      for (int i = 0; i < 64; i += 2) {
+        tc::fma2(p + i, c, c, -lse2, -lse2);
+        p[i] = tc::ex2(p[i]);
+        p[i + 1] = tc::ex2(p[i + 1]);
+      }
+      if (!(ok = wait(dp_full, j, a))) break;
+      tc::fence_after();
+      uint32_t w[32];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        float g[32];
+        tc::ld32(dp_at + lanes + cols + 32 * b, g);
+        tc::wait_ld();
+        tc::tie32(g);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          tc::add2(g + i, -delta, -delta);
+          tc::mul2(g + i, p[32 * b + i], p[32 * b + i + 1]);
+        }
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) g[i] = (32 * b + i < lim || 32 * b + i == self) ? g[i] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) w[16 * b + i / 2] = tc::pack2(g[i], g[i + 1]);
+      }
+      tc::st32(dp_at + lanes + cols, w);
+      tc::wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::arrive(ds_ready);
+    }
+    if (ok && wait(fin, 0, a)) {
+      tc::fence_after();
+#pragma unroll
+      for (int b = 0; b < DH / 64; ++b) {
+        const int col = half * (DH / 2) + 32 * b;
+        float g[32];
+        tc::ld32(dq_at + lanes + col, g);
+        tc::wait_ld();
+        tc::tie32(g);
+        if (live) store32(a.dq + pos * a.dq_stride + head * DH + col, g, a.scale);
+      }
+      tc::fence_before();
+    }
+  }
+  __syncthreads();
+  if (warp == 8) {
+    tc::fence_after();
+    tc::dealloc(tmem_at, 512);
+  }
+}
+
+// dk and dv of one key tile and key/value head, over the query heads that
+// share it and the query tiles that see it.  A thread holds one key and 64 of
+// the 128 queries (everything transposed: x^T = k q^T, v do^T).  p^T (bf16)
+// goes over x^T and multiplies do, then the next x^T is computed while
+// ds^T = p^T * (v do^T - delta) is formed; ds^T goes over v do^T and multiplies q.
+template <int DH>
+__global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_constant__ CUtensorMap mq,
+                                                                  const __grid_constant__ CUtensorMap mk,
+                                                                  const __grid_constant__ CUtensorMap mv,
+                                                                  const __grid_constant__ CUtensorMap mdo, AttnArgs a) {
+  constexpr int TB = tile_bytes<DH>();
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) uint64_t bars[10];
+  __shared__ uint32_t tmem_at;
+  __shared__ __align__(16) float row_lse[2][kTile], row_delta[2][kTile];
+  const int kv_head = int(blockIdx.x % unsigned(a.kv_heads));
+  const int64_t at = blockIdx.x / unsigned(a.kv_heads);
+  if (at >= *a.ntiles) return;
+  const Tile x = a.tiles[at];
+  const int group = a.heads / a.kv_heads;
+  int first;
+  const int nq = query_tiles(x, a.causal, first);
+  const int n = nq * group;
+  unsigned char* smem = align_smem(raw);
+  const uint32_t k_at = bulk::smem_addr(smem), v_at = k_at + TB, q_at = v_at + TB;  // then two stages of (q, do)
+  const uint32_t bar = bulk::smem_addr(bars);
+  const uint32_t k_full = bar, q_full = bar + 8, s_full = bar + 24, dp_full = bar + 32, p_ready = bar + 40,
+                 ds_ready = bar + 48, done = bar + 56, drain = bar + 64, fin = bar + 72;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 8) {
+    if (lane == 0) {
+      tc::prefetch_map(&mq), tc::prefetch_map(&mk), tc::prefetch_map(&mv), tc::prefetch_map(&mdo);
+      for (int i = 0; i < 10; ++i) bulk::mbar_init(bar + 8 * i, i == 5 || i == 6 ? 8 : 1);
+      bulk::fence_init();
+    }
+    __syncwarp();
+    tc::alloc(&tmem_at, 512);
+    tc::fence_before();
+  }
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t s_at = tmem_at, dp_at = tmem_at + 128, dv_at = tmem_at + 256, dk_at = tmem_at + 256 + DH;
+  auto query_tile = [&](int j) { return first + j % nq; };
+  auto query_head = [&](int j) { return kv_head * group + j / nq; };
+
+  if (warp == 8) {
+    int loaded = 0;
+    auto load_q = [&](int j) {
+      if (lane == 0) {
+        const uint32_t b = q_full + 8 * (j & 1), to = q_at + (j & 1) * 2 * TB;
+        const int y = x.begin + query_tile(j) * kTile;
+        bulk::arrive_expect_tx(b, 2 * TB);
+        load_tile<DH>(to, &mq, query_head(j), y, b);
+        load_tile<DH>(to + TB, &mdo, query_head(j), y, b);
+      }
+      loaded = j + 1;
+    };
+    auto query_ready = [&](int j) {
+      if (!wait(q_full + 8 * (j & 1), j >> 1, a)) return false;
+      const int valid = x.L - query_tile(j) * kTile;
+      if (valid < kTile) {
+        zero_rows<DH>(smem + TB * (2 + 2 * (j & 1)), valid);
+        zero_rows<DH>(smem + TB * (3 + 2 * (j & 1)), valid);
+      }
+      return true;
+    };
+    if (lane == 0) {
+      bulk::arrive_expect_tx(k_full, 2 * TB);
+      load_tile<DH>(k_at, &mk, kv_head, x.begin + x.t * kTile, k_full);
+      load_tile<DH>(v_at, &mv, kv_head, x.begin + x.t * kTile, k_full);
+    }
+    for (int j = 0; j < 2 && j < n; ++j) load_q(j);
+    bool ok = wait(k_full, 0, a) && query_ready(0);
+    if (ok && lane == 0) {
+      mma_rows<DH>(s_at, k_at, q_at);
+      tc::commit(s_full);
+      mma_rows<DH>(dp_at, v_at, q_at + TB);
+      tc::commit(dp_full);
+    }
+    __syncwarp();
+    for (int j = 0; ok && j < n; ++j) {
+      const uint32_t cur = q_at + (j & 1) * 2 * TB, nxt = q_at + ((j + 1) & 1) * 2 * TB;
+      if (j + 1 < n && !(ok = query_ready(j + 1))) break;
+      if (!(ok = wait(p_ready, j, a))) break;
+      tc::fence_after();
+      if (lane == 0) {
+        mma_cols<DH>(dv_at, s_at, s_at + 64, cur + TB, j != 0);
+        if (j + 1 < n) {  // x^T overwrites p^T: the products execute in the order they are issued
+          mma_rows<DH>(s_at, k_at, nxt);
+          tc::commit(s_full);
+        }
+      }
+      __syncwarp();
+      if (!(ok = wait(ds_ready, j, a))) break;
+      tc::fence_after();
+      if (lane == 0) {
+        mma_cols<DH>(dk_at, dp_at, dp_at + 64, cur, j != 0);
+        tc::commit(j + 1 < n ? done : fin);
+        if (j + 1 < n) {
+          mma_rows<DH>(dp_at, v_at, nxt + TB);
+          tc::commit(dp_full);
+        }
+      }
+      __syncwarp();
+      if (j + 2 < n) {
+        if (!(ok = wait(done, j, a))) break;
+        load_q(j + 2);
+      }
+    }
+    if (!ok) {
+      if (lane == 0) tc::commit(drain);
+      bulk::warp_wait(drain, 0, a.wait_ns);
+      bulk::warp_wait(k_full, 0, a.wait_ns);
+      for (int s = 0; s < 2; ++s)
+        if (loaded > s) bulk::warp_wait(q_full + 8 * s, ((loaded - 1 - s) >> 1) & 1, a.wait_ns);
+    }
+  } else {
+    const int r = threadIdx.x & 127, half = threadIdx.x >> 7;
+    const int key = x.t * kTile + r;
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t cols = 64 * half;
+    const float c = a.scale * kLog2e;
+    // lse (in powers of two) or delta of query r of tile j; queries past the sample's end weigh nothing
+    auto row_value = [&](int j) {
+      const int i = query_tile(j) * kTile + r;
+      const int64_t at = int64_t(query_head(j)) * a.T + x.begin + i;
+      if (half == 0) return i < x.L ? a.lse[at] * kLog2e : INFINITY;
+      return i < x.L ? a.delta[at] : 0.f;
+    };
+    auto put_value = [&](int j, float v) { (half == 0 ? row_lse : row_delta)[j & 1][r] = v; };
+    put_value(0, row_value(0));
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      // one barrier a tile: this tile's values are in, and the last tile's are read
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      float next = 0.f;
+      if (j + 1 < n) next = row_value(j + 1);
+      ok = ok && wait(s_full, j, a);
+      if (!ok) continue;  // every warp keeps meeting the barrier
+      tc::fence_after();
+      float p[64];
+      tc::ld32(s_at + lanes + cols, p);
+      tc::ld32(s_at + lanes + cols + 32, p + 32);
+      tc::wait_ld();
+      tc::tie32(p);
+      tc::tie32(p + 32);
+      const float4* ls = reinterpret_cast<const float4*>(&row_lse[j & 1][cols]);
+#pragma unroll
+      for (int i = 0; i < 64; i += 4) {
+        const float4 z = ls[i / 4];
+        tc::fma2(p + i, c, c, -z.x, -z.y);
+        tc::fma2(p + i + 2, c, c, -z.z, -z.w);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) p[i + q] = tc::ex2(p[i + q]);
+      }
+      const int i0 = query_tile(j) * kTile;
+      if (x.t * kTile + kTile > x.uih || (a.causal && i0 < x.t * kTile + kTile)) {
+        // query i0 + cols + i sees this key from `from` on, or only where it is the key's own position
+        const int self = key - i0 - int(cols);
+        const int from = key >= x.uih ? 128 : (a.causal ? self : -1);
+#pragma unroll
+        for (int i = 0; i < 64; ++i) p[i] = (i >= from || i == self) ? p[i] : 0.f;
+      }
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 64; i += 2) w[i / 2] = tc::pack2(p[i], p[i + 1]);
+      tc::st32(s_at + lanes + cols, w);
+      tc::wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::arrive(p_ready);
+      if (j + 1 < n) put_value(j + 1, next);
+      ok = wait(dp_full, j, a);
+      if (!ok) continue;
+      tc::fence_after();
+      const float4* dl = reinterpret_cast<const float4*>(&row_delta[j & 1][cols]);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        float g[32];
+        tc::ld32(dp_at + lanes + cols + 32 * b, g);
+        tc::wait_ld();
+        tc::tie32(g);
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const float4 z = dl[8 * b + i / 4];
+          tc::add2(g + i, -z.x, -z.y);
+          tc::add2(g + i + 2, -z.z, -z.w);
+          tc::mul2(g + i, p[32 * b + i], p[32 * b + i + 1]);
+          tc::mul2(g + i + 2, p[32 * b + i + 2], p[32 * b + i + 3]);
+          w[16 * b + i / 2] = tc::pack2(g[i], g[i + 1]);
+          w[16 * b + i / 2 + 1] = tc::pack2(g[i + 2], g[i + 3]);
+        }
+      }
+      tc::st32(dp_at + lanes + cols, w);
+      tc::wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::arrive(ds_ready);
+    }
+    if (ok && wait(fin, 0, a)) {
+      tc::fence_after();
+      const int64_t pos = int64_t(x.begin) + key;
+      __nv_bfloat16* to = half == 0 ? a.dv + pos * a.dv_stride : a.dk + pos * a.dk_stride;
+      const uint32_t from = half == 0 ? dv_at : dk_at;
+      const float f = half == 0 ? 1.f : a.scale;
+#pragma unroll
+      for (int b = 0; b < DH / 32; ++b) {
+        float g[32];
+        tc::ld32(from + lanes + 32 * b, g);
+        tc::wait_ld();
+        tc::tie32(g);
+        if (key < x.L) store32(to + kv_head * DH + 32 * b, g, f);
+      }
+      tc::fence_before();
+    }
+  }
+  __syncthreads();
+  if (warp == 8) {
+    tc::fence_after();
+    tc::dealloc(tmem_at, 512);
+  }
+}
+
+// ------------------------------------------------------------- host side
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static EncodeFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult got;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &got) == cudaSuccess &&
+        got == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeFn>(p);
+    else
+      cudaGetLastError();
+  });
+  return fn;
+}
+
+// Map of [T, width] bf16 with rows `stride` elements apart, in boxes of 128 rows of 64 columns.
+bool encode(CUtensorMap* map, const void* base, int64_t T, int64_t width, int64_t stride) {
+  EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {cuuint64_t(width), cuuint64_t(T)}, strides[1] = {cuuint64_t(stride) * 2};
+  const cuuint32_t box[2] = {64, kTile}, ones[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 fs_status check_attn(int64_t S, int64_t T, int32_t Hq, int32_t Hkv, int32_t Dh, float scale, const int64_t* offsets,
@@ -193,7 +929,26 @@ fs_status check_rows(const void* p, int64_t stride, int32_t heads, int32_t Dh) {
   return aligned(p, 16) && stride % 8 == 0 ? FS_OK : FS_ERR_ALIGNMENT;
 }
 
-unsigned warps_grid(int64_t warps) { return unsigned((warps + 3) / 4); }
+int64_t most_tiles(int64_t T, int64_t S) { return T / kTile + (S < T ? S : T); }
+
+struct AttnWs {
+  int32_t* ntiles = nullptr;
+  Tile *by_query = nullptr, *by_key = nullptr;
+  float* delta = nullptr;
+};
+
+template <class Ws>
+void take_attn(int64_t T, int64_t S, int32_t Hq, Ws& ws, AttnWs& W) {
+  W.ntiles = ws.template take<int32_t>(1);
+  W.by_query = ws.template take<Tile>(size_t(most_tiles(T, S)));
+  W.by_key = ws.template take<Tile>(size_t(most_tiles(T, S)));
+  W.delta = ws.template take<float>(size_t(Hq) * size_t(T));
+}
+
+template <class K>
+void raise_smem(K kern, int bytes) {
+  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
 
 }  // namespace
 }  // namespace fs
@@ -203,7 +958,10 @@ using namespace fs;
 extern "C" size_t fs_jagged_attn_workspace_size(int64_t T, int64_t S, int32_t heads, int32_t kv_heads,
                                                 int32_t head_dim) {
   if (T < 0 || S < 0 || heads < 1 || kv_heads < 1 || (head_dim != 64 && head_dim != 128)) return 0;
-  return 256;
+  WsCounter c;
+  AttnWs W;
+  take_attn(T, S, heads, c, W);
+  return c.used;
 }
 
 extern "C" fs_status fs_jagged_attn(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
@@ -221,16 +979,29 @@ extern "C" fs_status fs_jagged_attn(const void* q, int64_t q_stride, const void*
       (s = check_rows(out, int64_t(heads) * head_dim, heads, head_dim)) != FS_OK)
     return s;
   if (!ws || ws_bytes < fs_jagged_attn_workspace_size(T, S, heads, kv_heads, head_dim)) return FS_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return FS_ERR_ALIGNMENT;
+  if (most_tiles(T, S) * heads > INT32_MAX) return FS_ERR_INVALID_ARG;
+  WsCursor cur(ws, ws_bytes);
+  AttnWs W;
+  take_attn(T, S, heads, cur, W);
+  CUtensorMap mq, mk, mv;
+  if (!encode(&mq, q, T, int64_t(heads) * head_dim, q_stride) || !encode(&mk, k, T, int64_t(kv_heads) * head_dim, k_stride) ||
+      !encode(&mv, v, T, int64_t(kv_heads) * head_dim, v_stride))
+    return FS_ERR_CUDA;
   AttnArgs a{};
-  using B = __nv_bfloat16;
-  a.q = static_cast<const B*>(q), a.k = static_cast<const B*>(k), a.v = static_cast<const B*>(v);
-  a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
-  a.o = static_cast<B*>(out);
-  a.offsets = offsets, a.S = S, a.T = T, a.Hq = heads, a.Hkv = kv_heads, a.cand = cand_len, a.causal = causal;
-  a.scale = scale, a.lse = lse, a.err = err;
-  attn_check_kernel<<<unsigned((S + 127) / 128), 128, 0, st>>>(a);
-  if (head_dim == 64) attn_fwd_kernel<2><<<warps_grid(T * heads), 128, 0, st>>>(a);
-  else attn_fwd_kernel<4><<<warps_grid(T * heads), 128, 0, st>>>(a);
+  a.ntiles = W.ntiles, a.tiles = W.by_query;
+  a.heads = heads, a.kv_heads = kv_heads, a.T = T, a.causal = causal != 0, a.scale = scale;
+  a.o = static_cast<__nv_bfloat16*>(out), a.lse = lse, a.err = err;
+  a.wait_ns = uint64_t(spin_limit()) * 256u;
+  attn_plan_kernel<<<1, kPlanThreads, 0, st>>>(offsets, S, T, cand_len, a.causal, W.ntiles, W.by_query, nullptr, err);
+  const unsigned grid = unsigned(most_tiles(T, S) * heads);
+  if (head_dim == 64) {
+    raise_smem(attn_fwd_kernel<64>, fwd_smem<64>());
+    attn_fwd_kernel<64><<<grid, kFwdThreads, fwd_smem<64>(), st>>>(mq, mk, mv, a);
+  } else {
+    raise_smem(attn_fwd_kernel<128>, fwd_smem<128>());
+    attn_fwd_kernel<128><<<grid, kFwdThreads, fwd_smem<128>(), st>>>(mq, mk, mv, a);
+  }
   count_launch(2);
   return launch_status();
 }
@@ -247,7 +1018,7 @@ extern "C" fs_status fs_jagged_attn_backward(const void* q, int64_t q_stride, co
   fs_status s = check_attn(S, T, heads, kv_heads, head_dim, scale, offsets, cand_len, lse, err);
   if (s != FS_OK) return s;
   if (S == 0 || T == 0) return FS_OK;
-  const int64_t ow = int64_t(heads) * head_dim;
+  const int64_t ow = int64_t(heads) * head_dim, kw = int64_t(kv_heads) * head_dim;
   if ((s = check_rows(q, q_stride, heads, head_dim)) != FS_OK || (s = check_rows(k, k_stride, kv_heads, head_dim)) != FS_OK ||
       (s = check_rows(v, v_stride, kv_heads, head_dim)) != FS_OK || (s = check_rows(out, ow, heads, head_dim)) != FS_OK ||
       (s = check_rows(dout, ow, heads, head_dim)) != FS_OK || (s = check_rows(dq, dq_stride, heads, head_dim)) != FS_OK ||
@@ -255,22 +1026,37 @@ extern "C" fs_status fs_jagged_attn_backward(const void* q, int64_t q_stride, co
       (s = check_rows(dv, dv_stride, kv_heads, head_dim)) != FS_OK)
     return s;
   if (!ws || ws_bytes < fs_jagged_attn_workspace_size(T, S, heads, kv_heads, head_dim)) return FS_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return FS_ERR_ALIGNMENT;
+  if (most_tiles(T, S) * heads > INT32_MAX) return FS_ERR_INVALID_ARG;
+  WsCursor cur(ws, ws_bytes);
+  AttnWs W;
+  take_attn(T, S, heads, cur, W);
+  CUtensorMap mq, mk, mv, mdo;
+  if (!encode(&mq, q, T, ow, q_stride) || !encode(&mk, k, T, kw, k_stride) || !encode(&mv, v, T, kw, v_stride) ||
+      !encode(&mdo, dout, T, ow, ow))
+    return FS_ERR_CUDA;
   AttnArgs a{};
-  using B = __nv_bfloat16;
-  a.q = static_cast<const B*>(q), a.k = static_cast<const B*>(k), a.v = static_cast<const B*>(v);
-  a.out = static_cast<const B*>(out), a.dout = static_cast<const B*>(dout);
-  a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
-  a.dq = static_cast<B*>(dq), a.dk = static_cast<B*>(dk), a.dv = static_cast<B*>(dv);
+  a.ntiles = W.ntiles;
+  a.heads = heads, a.kv_heads = kv_heads, a.T = T, a.causal = causal != 0, a.scale = scale;
+  a.out = static_cast<const __nv_bfloat16*>(out), a.dout = static_cast<const __nv_bfloat16*>(dout);
+  a.lse = const_cast<float*>(lse), a.delta = W.delta, a.err = err;
+  a.dq = static_cast<__nv_bfloat16*>(dq), a.dk = static_cast<__nv_bfloat16*>(dk), a.dv = static_cast<__nv_bfloat16*>(dv);
   a.dq_stride = dq_stride, a.dk_stride = dk_stride, a.dv_stride = dv_stride;
-  a.offsets = offsets, a.S = S, a.T = T, a.Hq = heads, a.Hkv = kv_heads, a.cand = cand_len, a.causal = causal;
-  a.scale = scale, a.lse = const_cast<float*>(lse), a.err = err;
-  attn_check_kernel<<<unsigned((S + 127) / 128), 128, 0, st>>>(a);
+  a.wait_ns = uint64_t(spin_limit()) * 256u;
+  attn_plan_kernel<<<1, kPlanThreads, 0, st>>>(offsets, S, T, cand_len, a.causal, W.ntiles, W.by_query, W.by_key, err);
+  const unsigned gq = unsigned(most_tiles(T, S) * heads), gk = unsigned(most_tiles(T, S) * kv_heads);
+  AttnArgs b = a;
+  a.tiles = W.by_query, b.tiles = W.by_key;
   if (head_dim == 64) {
-    attn_dq_kernel<2><<<warps_grid(T * heads), 128, 0, st>>>(a);
-    attn_dkv_kernel<2><<<warps_grid(T * kv_heads), 128, 0, st>>>(a);
+    raise_smem(attn_dq_kernel<64>, bwd_smem<64>());
+    raise_smem(attn_dkv_kernel<64>, bwd_smem<64>());
+    attn_dq_kernel<64><<<gq, kBwdThreads, bwd_smem<64>(), st>>>(mq, mk, mv, mdo, a);
+    attn_dkv_kernel<64><<<gk, kBwdThreads, bwd_smem<64>(), st>>>(mq, mk, mv, mdo, b);
   } else {
-    attn_dq_kernel<4><<<warps_grid(T * heads), 128, 0, st>>>(a);
-    attn_dkv_kernel<4><<<warps_grid(T * kv_heads), 128, 0, st>>>(a);
+    raise_smem(attn_dq_kernel<128>, bwd_smem<128>());
+    raise_smem(attn_dkv_kernel<128>, bwd_smem<128>());
+    attn_dq_kernel<128><<<gq, kBwdThreads, bwd_smem<128>(), st>>>(mq, mk, mv, mdo, a);
+    attn_dkv_kernel<128><<<gk, kBwdThreads, bwd_smem<128>(), st>>>(mq, mk, mv, mdo, b);
   }
   count_launch(3);
   return launch_status();
