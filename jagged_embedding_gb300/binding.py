@@ -137,11 +137,11 @@ def lib():
 # ------------------------------------------------------------------ helpers
 
 def _ptr(t):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(device):
-    return C.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _need(t, dtype, name, numel=None):
@@ -596,8 +596,8 @@ def fs_emb_update_sorted(table, state, grads, T, ws, optim, lr, eps=0.0, phase=P
 
 def _same(t, shape, dtype, name, device):
     """An output or second operand: exactly this shape and type, contiguous, on the same device."""
-    if t.device != device or tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
-        raise FsError(1, f"{name} must be a contiguous {tuple(shape)} tensor of {dtype} on {device}")
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise FsError(1, f"{name} must be a contiguous {shape} tensor of {dtype} on {device}")
 
 
 def fs_emb_lookup_scaled(table, ids, scale=1.0, out=None, out_dtype=None, err=None, T=None):
@@ -706,11 +706,12 @@ def fs_rmsnorm_backward(dy, h, gamma, rstd, dsum=None, dh=None, dgamma=None, ws=
 
 def _rows(t, T, heads, dim, name, device):
     """[T, heads, dim] bf16 whose rows are contiguous (a slice of a wider row is fine); returns the row stride."""
-    if t.device != device or t.dtype != torch.bfloat16 or tuple(t.shape) != (T, heads, dim):
+    if t.shape != (T, heads, dim) or t.dtype != torch.bfloat16 or t.device != device:
         raise FsError(1, f"{name} must be a ({T}, {heads}, {dim}) tensor of torch.bfloat16 on {device}")
-    if (dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim):
+    s = t.stride()
+    if (dim > 1 and s[2] != 1) or (heads > 1 and s[1] != dim):
         raise FsError(1, f"{name}: the heads of a position must be contiguous")
-    return t.stride(0) if T > 1 else max(t.stride(0), heads * dim)
+    return s[0] if T > 1 else max(s[0], heads * dim)
 
 
 def jagged_attn_workspace_size(T, S, heads, kv_heads, head_dim):

@@ -20,6 +20,7 @@
 // twice (7 products where a pass with atomic sums of dq needs 5).
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "fs_common.cuh"
@@ -945,10 +946,17 @@ void take_attn(int64_t T, int64_t S, int32_t Hq, Ws& ws, AttnWs& W) {
   W.delta = ws.template take<float>(size_t(Hq) * size_t(T));
 }
 
+// Allows a kernel its shared memory, once per device (`done` holds a bit for each).
 template <class K>
-void raise_smem(K kern, int bytes) {
-  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+void raise_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
+  if (bit && (done.load(std::memory_order_relaxed) & bit)) return;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess) done.fetch_or(bit);
 }
+
+std::atomic<uint64_t> g_fwd_ready[2], g_bwd_ready[2][2];
 
 }  // namespace
 }  // namespace fs
@@ -996,10 +1004,10 @@ extern "C" fs_status fs_jagged_attn(const void* q, int64_t q_stride, const void*
   attn_plan_kernel<<<1, kPlanThreads, 0, st>>>(offsets, S, T, cand_len, a.causal, W.ntiles, W.by_query, nullptr, err);
   const unsigned grid = unsigned(most_tiles(T, S) * heads);
   if (head_dim == 64) {
-    raise_smem(attn_fwd_kernel<64>, fwd_smem<64>());
+    raise_smem(attn_fwd_kernel<64>, fwd_smem<64>(), g_fwd_ready[0]);
     attn_fwd_kernel<64><<<grid, kFwdThreads, fwd_smem<64>(), st>>>(mq, mk, mv, a);
   } else {
-    raise_smem(attn_fwd_kernel<128>, fwd_smem<128>());
+    raise_smem(attn_fwd_kernel<128>, fwd_smem<128>(), g_fwd_ready[1]);
     attn_fwd_kernel<128><<<grid, kFwdThreads, fwd_smem<128>(), st>>>(mq, mk, mv, a);
   }
   count_launch(2);
@@ -1048,13 +1056,13 @@ extern "C" fs_status fs_jagged_attn_backward(const void* q, int64_t q_stride, co
   AttnArgs b = a;
   a.tiles = W.by_query, b.tiles = W.by_key;
   if (head_dim == 64) {
-    raise_smem(attn_dq_kernel<64>, bwd_smem<64>());
-    raise_smem(attn_dkv_kernel<64>, bwd_smem<64>());
+    raise_smem(attn_dq_kernel<64>, bwd_smem<64>(), g_bwd_ready[0][0]);
+    raise_smem(attn_dkv_kernel<64>, bwd_smem<64>(), g_bwd_ready[0][1]);
     attn_dq_kernel<64><<<gq, kBwdThreads, bwd_smem<64>(), st>>>(mq, mk, mv, mdo, a);
     attn_dkv_kernel<64><<<gk, kBwdThreads, bwd_smem<64>(), st>>>(mq, mk, mv, mdo, b);
   } else {
-    raise_smem(attn_dq_kernel<128>, bwd_smem<128>());
-    raise_smem(attn_dkv_kernel<128>, bwd_smem<128>());
+    raise_smem(attn_dq_kernel<128>, bwd_smem<128>(), g_bwd_ready[1][0]);
+    raise_smem(attn_dkv_kernel<128>, bwd_smem<128>(), g_bwd_ready[1][1]);
     attn_dq_kernel<128><<<gq, kBwdThreads, bwd_smem<128>(), st>>>(mq, mk, mv, mdo, a);
     attn_dkv_kernel<128><<<gk, kBwdThreads, bwd_smem<128>(), st>>>(mq, mk, mv, mdo, b);
   }

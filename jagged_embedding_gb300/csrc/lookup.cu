@@ -13,14 +13,15 @@ namespace {
 constexpr int kLookupThreads = 256;
 
 // 32 / LPR rows per warp instruction (LPR lanes a row, VEC elements a lane),
-// U rows in flight per lane; the next iteration's IDs are loaded before this
-// iteration's rows.  Rows of more than LPR * VEC elements take several steps.
+// U rows in flight per lane, held as loaded; the next iteration's IDs are
+// loaded before this iteration's rows.  Rows of more than LPR * VEC elements
+// take several steps.
 // Bound by HBM: 8 B of ID, one table row (distinct rows once, the others from
-// L2) and one output row per position, 2 multiplies per 8 bytes.
+// L2) and one output row per position.
 template <class EI, class EO, int VEC, int LPR>
-__global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const void* __restrict__ table, int64_t R, int32_t dim,
-                                                                const int64_t* __restrict__ ids, int64_t T, float scale,
-                                                                void* __restrict__ out, int32_t* err) {
+__global__ void __launch_bounds__(kLookupThreads, 4) lookup_kernel(const void* __restrict__ table, int64_t R, int32_t dim,
+                                                                   const int64_t* __restrict__ ids, int64_t T,
+                                                                   float scale, void* __restrict__ out, int32_t* err) {
   constexpr int RPI = 32 / LPR;
   constexpr int U = RPI * 8 <= 32 ? 8 : 32 / RPI;
   constexpr int RPW = RPI * U;
@@ -29,35 +30,32 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const void* __re
   const int64_t nwarps = (int64_t(gridDim.x) * blockDim.x) >> 5;
   const int64_t stride = nwarps * RPW;
   int64_t p0 = ((int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5) * RPW;
-  auto load_id = [&](int64_t p) { return (lane < RPW && p + lane < T) ? __ldcs(ids + p + lane) : int64_t(0); };
+  auto load_id = [&](int64_t p) { return (lane < RPW && p + lane < T) ? __ldcs(ids + p + lane) : int64_t(-1); };
   int64_t next = load_id(p0);
   for (; p0 < T; p0 += stride) {
     int64_t id = next;
     next = load_id(p0 + stride);
-    if (lane < RPW && p0 + lane < T && uint64_t(id) >= uint64_t(R)) {
-      set_err(err, FS_ERR_ID_RANGE);
-      id = -1;
+    if (uint64_t(id) >= uint64_t(R)) {
+      if (lane < RPW && p0 + lane < T) set_err(err, FS_ERR_ID_RANGE);
+      id = -1;  // a row of zeros
     }
-    int64_t row[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) row[u] = __shfl_sync(0xffffffffu, id, u * RPI + sub);
-    for (int c = c0; c < dim; c += LPR * VEC) {
-      float x[U][VEC];
+    for (int c = c0; c - c0 < dim; c += LPR * VEC) {  // (the same steps for every lane: the shuffles need them all)
+      Raw<EI, VEC> r[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const bool live = p0 + u * RPI + sub < T && row[u] >= 0;
-        if (live) load_vec<EI, VEC, false>(table, row[u] * dim + c, x[u]);
-        else
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) x[u][k] = 0.f;  // an ID out of range gives a row of zeros
+        const int64_t row = __shfl_sync(0xffffffffu, id, u * RPI + sub);
+        memset(&r[u], 0, sizeof(r[u]));
+        if (row >= 0 && c < dim) fetch<false>(r[u], table, row * dim + c);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t p = p0 + u * RPI + sub;
-        if (p < T) {
+        if (p < T && c < dim) {
+          float x[VEC];
+          unpack(r[u], x);
 #pragma unroll
-          for (int k = 0; k < VEC; ++k) x[u][k] *= scale;
-          store_vec<EO, VEC, true>(out, p * dim + c, x[u]);
+          for (int k = 0; k < VEC; ++k) x[k] *= scale;
+          store_vec<EO, VEC, true>(out, p * dim + c, x);
         }
       }
     }

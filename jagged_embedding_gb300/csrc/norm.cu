@@ -69,8 +69,9 @@ __device__ __forceinline__ void load_gamma(const float* gamma, int c, float (&w)
 }
 
 // G threads per row, each with NC chunks of VEC elements (chunk j of thread g
-// starts at (j * G + g) * VEC).
-template <class E, class EY, int VEC, int G, int NC>
+// starts at (j * G + g) * VEC).  The next row's chunks are loaded, and held as
+// loaded, before the current row is worked on.
+template <class E, class EY, int VEC, int G, int NC, bool RES>
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(const void* x, const void* res, int64_t T,
                                                             int32_t dim, const float* __restrict__ gamma, float eps,
                                                             void* sum_out /* may be x or res */, void* __restrict__ y,
@@ -80,6 +81,18 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const void* x, const
   constexpr int RPB = kNormThreads / G;
   const int g = threadIdx.x % G;
   const int64_t step = int64_t(gridDim.x) * RPB;
+  Raw<E, VEC> nx[NC], nr[NC];
+  auto load_row = [&](int64_t row) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const int c = (j * G + g) * VEC;
+      if (row < T && c < dim) {
+        fetch<true>(nx[j], x, row * dim + c);
+        if (RES) fetch<true>(nr[j], res, row * dim + c);
+      }
+    }
+  };
+  load_row(int64_t(blockIdx.x) * RPB + threadIdx.x / G);
   // every thread of a warp or block runs the same iterations (its row may lie past the end)
   for (int64_t base = int64_t(blockIdx.x) * RPB; base < T; base += step) {
     const int64_t row = base + threadIdx.x / G;
@@ -89,34 +102,34 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const void* x, const
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int c = (j * G + g) * VEC;
+      const bool in = live && c < dim;
+      if (in) {
+        unpack(nx[j], h[j]);
+        if constexpr (RES) {
+          float r[VEC];
+          unpack(nr[j], r);
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) h[j][k] = 0.f;
-      if (live && c < dim) load_vec<E, VEC, true>(x, row * dim + c, h[j]);
-    }
-    if (res) {
-      float r[NC][VEC];
+          for (int k = 0; k < VEC; ++k) h[j][k] += r[k];
+          if constexpr (E::kBytes == 2) {  // the norm is of the sum as it is stored
 #pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        const int c = (j * G + g) * VEC;
-        if (live && c < dim) load_vec<E, VEC, true>(res, row * dim + c, r[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        const int c = (j * G + g) * VEC;
-        if (live && c < dim) {
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) {
-            h[j][k] += r[j][k];
-            if constexpr (E::kBytes == 2) h[j][k] = __bfloat162float(__float2bfloat16_rn(h[j][k]));
+            for (int k = 0; k < VEC; ++k) h[j][k] = __bfloat162float(__float2bfloat16_rn(h[j][k]));
           }
-          store_vec<E, VEC, false>(sum_out, row * dim + c, h[j]);
         }
-      }
-    }
+      } else {
 #pragma unroll
-    for (int j = 0; j < NC; ++j)
+        for (int k = 0; k < VEC; ++k) h[j][k] = 0.f;
+      }
 #pragma unroll
       for (int k = 0; k < VEC; ++k) ss = fmaf(h[j][k], h[j][k], ss);
+    }
+    load_row(row + step);
+    if constexpr (RES) {
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const int c = (j * G + g) * VEC;
+        if (live && c < dim) store_vec<E, VEC, false>(sum_out, row * dim + c, h[j]);
+      }
+    }
     ss = row_all<G>(ss, Add{}, red, turn);
     const float rs = 1.f / sqrtf(ss / float(dim) + eps);
     if (live && g == 0 && rstd) rstd[row] = rs;
@@ -139,13 +152,17 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const void* x, const
       top = row_all<G>(top, Max{}, red, turn);
       const float s = top / 448.f;
       if (live && g == 0) y_scale[row] = s;
-      const float d = s > 0.f ? s : 1.f;  // a row of zeros stays zeros, its scale 0
+      // one reciprocal a row: q is e4m3 of y / s but for quotients within an fp32 ulp or two of the middle
+      // between two e4m3 values.  A row of zeros stays zeros, its scale 0; a scale too small for its
+      // reciprocal (below 2^-126) divides.
+      const bool tiny = s < 1.1754944e-38f;
+      const float f = s > 0.f ? (tiny ? s : 1.f / s) : 1.f;
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
         const int c = (j * G + g) * VEC;
         if (live && c < dim) {
 #pragma unroll
-          for (int k = 0; k < VEC; ++k) h[j][k] = h[j][k] / d;
+          for (int k = 0; k < VEC; ++k) h[j][k] = tiny && s > 0.f ? h[j][k] / f : h[j][k] * f;
           store_vec<EY, VEC, true>(y, row * dim + c, h[j]);
         }
       }
@@ -157,7 +174,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const void* x, const
 // in registers over its rows, a block adds its threads' shares in thread
 // order, and gamma_sum_kernel adds the blocks' shares in block order: the
 // result does not depend on the order in which blocks run.
-template <class E, int VEC, int G, int NC>
+template <class E, int VEC, int G, int NC, bool SUM>
 __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(const void* dy, const void* dsum, const void* hin,
                                                                 int64_t T, int32_t dim, const float* __restrict__ gamma,
                                                                 const float* __restrict__ rstd,
@@ -174,28 +191,36 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(const void* dy, 
   for (int j = 0; j < NC; ++j)
 #pragma unroll
     for (int k = 0; k < VEC; ++k) dg[j][k] = 0.f;
-  for (int64_t base = int64_t(blockIdx.x) * RPB; base < T; base += step) {
-    const int64_t row = base + threadIdx.x / G;
-    const bool live = row < T;
-    float n[NC][VEC], w[NC][VEC], d[NC][VEC];
-    const float rs = live ? __ldcs(rstd + row) : 0.f;
+  Raw<E, VEC> nh[NC], ny[NC], nd[NC];
+  float nrs = 0.f;
+  auto load_row = [&](int64_t row) {
+    if (row < T) nrs = __ldcs(rstd + row);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int c = (j * G + g) * VEC;
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) n[j][k] = w[j][k] = d[j][k] = 0.f;
-      if (live && c < dim) {
-        load_vec<E, VEC, true>(hin, row * dim + c, n[j]);
-        load_vec<E, VEC, true>(dy, row * dim + c, w[j]);
-        if (dsum) load_vec<E, VEC, true>(dsum, row * dim + c, d[j]);
+      if (row < T && c < dim) {
+        fetch<true>(nh[j], hin, row * dim + c);
+        fetch<true>(ny[j], dy, row * dim + c);
+        if (SUM) fetch<true>(nd[j], dsum, row * dim + c);
       }
     }
+  };
+  load_row(int64_t(blockIdx.x) * RPB + threadIdx.x / G);
+  for (int64_t base = int64_t(blockIdx.x) * RPB; base < T; base += step) {
+    const int64_t row = base + threadIdx.x / G;
+    const bool live = row < T;
+    const float rs = nrs;
+    float n[NC][VEC], w[NC][VEC];
+    Raw<E, VEC> d[NC];
     float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int c = (j * G + g) * VEC;
+      d[j] = nd[j];
       if (live && c < dim) {
         float gm[VEC];
+        unpack(nh[j], n[j]);
+        unpack(ny[j], w[j]);
         load_gamma<VEC>(gamma, c, gm);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
@@ -206,14 +231,22 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(const void* dy, 
         }
       }
     }
+    load_row(row + step);
     dot = row_all<G>(dot, Add{}, red, turn) / float(dim);
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       const int c = (j * G + g) * VEC;
       if (live && c < dim) {
+        float v[VEC];
+        if constexpr (SUM) {
+          unpack(d[j], v);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) d[j][k] += rs * (w[j][k] - n[j][k] * dot);
-        store_vec<E, VEC, true>(dh, row * dim + c, d[j]);
+          for (int k = 0; k < VEC; ++k) v[k] += rs * (w[j][k] - n[j][k] * dot);
+        } else {
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) v[k] = rs * (w[j][k] - n[j][k] * dot);
+        }
+        store_vec<E, VEC, true>(dh, row * dim + c, v);
       }
     }
   }
@@ -316,8 +349,13 @@ extern "C" fs_status fs_rmsnorm(const void* x, const void* res, int64_t T, int32
     constexpr int VEC = decltype(v)::value;
     return pick_shape<VEC>(dim, [&](auto gg, auto nc) {
       constexpr int G = decltype(gg)::value, NC = decltype(nc)::value;
-      norm_kernel<decltype(e), decltype(ey), VEC, G, NC><<<norm_grid(T, kNormThreads / G), kNormThreads, 0, st>>>(
-          x, res, T, dim, gamma, eps, sum_out, y, y_scale, rstd);
+      const int grid = norm_grid(T, kNormThreads / G);
+      if (res)
+        norm_kernel<decltype(e), decltype(ey), VEC, G, NC, true><<<grid, kNormThreads, 0, st>>>(
+            x, res, T, dim, gamma, eps, sum_out, y, y_scale, rstd);
+      else
+        norm_kernel<decltype(e), decltype(ey), VEC, G, NC, false><<<grid, kNormThreads, 0, st>>>(
+            x, res, T, dim, gamma, eps, sum_out, y, y_scale, rstd);
     });
   };
   using std::integral_constant;
@@ -371,8 +409,12 @@ extern "C" fs_status fs_rmsnorm_backward(const void* dy, const void* dsum, const
       constexpr int RPB = kNormThreads / G;
       blocks = bwd_grid(T, RPB);
       const size_t sm = RPB > 1 ? size_t(RPB) * dim * sizeof(float) : 0;  // at most 32 rows of 64 columns, 8 of 512
-      norm_bwd_kernel<decltype(e), VEC, G, NC><<<blocks, kNormThreads, sm, st>>>(dy, dsum, h, T, dim, gamma, rstd, dh,
-                                                                                part);
+      if (dsum)
+        norm_bwd_kernel<decltype(e), VEC, G, NC, true><<<blocks, kNormThreads, sm, st>>>(dy, dsum, h, T, dim, gamma,
+                                                                                         rstd, dh, part);
+      else
+        norm_bwd_kernel<decltype(e), VEC, G, NC, false><<<blocks, kNormThreads, sm, st>>>(dy, dsum, h, T, dim, gamma,
+                                                                                          rstd, dh, part);
     });
   };
   using std::integral_constant;

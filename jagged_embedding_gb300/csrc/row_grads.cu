@@ -119,14 +119,14 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(const uint32_t* __r
 // ------------------------------------------------------------- small batches
 
 // Sort, numbering and the count of a batch of at most 1024 * ITEMS entries by
-// one block: keys in registers, stable counting passes of `bits` (at most 8)
+// one block: keys in registers, stable counting passes of at most 10
 // bits over shared memory.  An ID out of range takes the key 2^kb - 1 >= R,
 // sorts last and is dropped.
-constexpr int kSmallThreads = 1024, kSmallWarps = kSmallThreads / 32;
+constexpr int kSmallThreads = 1024, kSmallWarps = kSmallThreads / 32, kSmallBins = 1024;
 constexpr int64_t kSmallMax = kSmallThreads * 8;
 template <int ITEMS>
 constexpr size_t small_smem() {
-  return (size_t(kSmallThreads) * ITEMS * 2 + kSmallWarps * 256 + 256 + 64) * sizeof(uint32_t);
+  return (size_t(kSmallThreads) * ITEMS * 2 + size_t(kSmallWarps + 1) * kSmallBins + 64) * sizeof(uint32_t);
 }
 
 template <int ITEMS>
@@ -136,9 +136,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_sort_kernel(const int6
   extern __shared__ uint32_t sm[];
   uint32_t* keys = sm;
   uint32_t* vals = keys + kSmallThreads * ITEMS;
-  uint32_t* hist = vals + kSmallThreads * ITEMS;  // [warps][256]
-  uint32_t* dstart = hist + kSmallWarps * 256;    // [256]
-  uint32_t* red = dstart + 256;                   // [64]
+  uint32_t* hist = vals + kSmallThreads * ITEMS;  // [warps][digits]
+  uint32_t* dstart = hist + kSmallWarps * kSmallBins;  // [digits]
+  uint32_t* red = dstart + kSmallBins;                 // [64]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   auto slot = [&](int i) { return warp * 32 * ITEMS + i * 32 + lane; };  // slot order = item order
   const uint32_t bad = uint32_t((uint64_t(1) << kb) - 1);
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_sort_kernel(const int6
       }
     }
   }
-  const int passes = (kb + 7) / 8, bits = (kb + passes - 1) / passes, nb = 1 << bits;
+  const int passes = (kb + 9) / 10, bits = (kb + passes - 1) / passes, nb = 1 << bits;
   for (int pass = 0; pass < passes; ++pass) {
     const int shift = bits * pass;
     for (int j = threadIdx.x; j < kSmallWarps * nb; j += kSmallThreads) hist[j] = 0u;
@@ -179,28 +179,17 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_sort_kernel(const int6
       __syncwarp();
     }
     __syncthreads();
-    uint32_t tot = 0, x = 0;
-    if (threadIdx.x < 256) {
-      if (int(threadIdx.x) < nb)
-        for (int w = 0; w < kSmallWarps; ++w) {
-          const uint32_t c = hist[w * nb + threadIdx.x];
-          hist[w * nb + threadIdx.x] = tot;
-          tot += c;
-        }
-      x = tot;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+    // thread d: digit d's entries, exclusive over the warps, then over the digits
+    uint32_t tot = 0;
+    if (int(threadIdx.x) < nb)
+      for (int w = 0; w < kSmallWarps; ++w) {
+        const uint32_t c = hist[w * nb + threadIdx.x];
+        hist[w * nb + threadIdx.x] = tot;
+        tot += c;
       }
-      if (lane == 31) red[warp] = x;
-    }
-    __syncthreads();
-    if (threadIdx.x < 256) {
-      uint32_t b = 0;
-      for (int w = 0; w < warp; ++w) b += red[w];
-      dstart[threadIdx.x] = b + x - tot;
-    }
+    uint32_t all;
+    const uint32_t first = block_exclusive_scan<uint32_t>(tot, red, &all);
+    if (int(threadIdx.x) < nb) dstart[threadIdx.x] = first;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i)
@@ -258,12 +247,17 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_sort_kernel(const int6
 constexpr int kRedThreads = 256, kRedRows = 8;  // dout rows in flight per lane
 
 // LPR lanes (VEC columns each) per tile of 2^chunk_log2 sorted entries;
-// blockIdx.y picks LPR * VEC columns of wider rows.
+// blockIdx.y picks LPR * VEC columns of wider rows.  kRedRows dout rows are in
+// flight per lane, held as loaded; the next step's keys and positions are
+// loaded before this step's rows.  (The key and position arrays are padded to
+// 64 entries, so a step's vector loads stay inside them.)
 template <class EI, class EO, int VEC, int LPR>
-__global__ void __launch_bounds__(kRedThreads) grad_reduce_kernel(
+__global__ void __launch_bounds__(kRedThreads, 3) grad_reduce_kernel(
     const uint32_t* __restrict__ keys, const uint32_t* __restrict__ vals, const int64_t* __restrict__ n_dev,
     const uint32_t* __restrict__ before, int chunk_log2, const void* __restrict__ dout, int32_t dim, float scale,
     void* __restrict__ grads, int64_t cap, float* __restrict__ part_head, float* __restrict__ part_tail) {
+  constexpr int SV = VEC * EO::kBytes > 16 ? VEC / 2 : VEC;  // columns of one store of a finished row
+  constexpr int PV = VEC > 4 ? 4 : VEC;                      // and of a partial one
   const int64_t n = *n_dev;
   const int chunk = 1 << chunk_log2;
   const int64_t t = (int64_t(blockIdx.x) * kRedThreads + threadIdx.x) / LPR;
@@ -272,41 +266,62 @@ __global__ void __launch_bounds__(kRedThreads) grad_reduce_kernel(
   const int c = (int(blockIdx.y) * LPR + int(threadIdx.x % LPR)) * VEC;
   if (c >= dim) return;
   const int m = n - s0 < chunk ? int(n - s0) : chunk;
-  const uint32_t* tk = keys + s0;
-  const uint32_t* tv = vals + s0;
+  struct Eight {
+    uint32_t x[8];
+  };
+  auto load8 = [](const uint32_t* p) {
+    Eight e;
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    e.x[0] = a.x, e.x[1] = a.y, e.x[2] = a.z, e.x[3] = a.w, e.x[4] = b.x, e.x[5] = b.y, e.x[6] = b.z, e.x[7] = b.w;
+    return e;
+  };
+  Eight nk = load8(keys + s0), nv = load8(vals + s0);
   int64_t u = before[t];
-  bool from_prev = s0 > 0 && tk[-1] == tk[0];  // the tile's first row began in an earlier tile
+  bool from_prev = s0 > 0 && keys[s0 - 1] == nk.x[0];  // the tile's first row began in an earlier tile
   if (from_prev) --u;
   float acc[VEC];
 #pragma unroll
   for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+  auto partial = [&](float* part) {
+#pragma unroll
+    for (int k = 0; k < VEC; k += PV) {
+      float x[PV];
+#pragma unroll
+      for (int i = 0; i < PV; ++i) x[i] = acc[k + i];
+      store_vec<F32, PV, false>(part, t * dim + c + k, x);
+    }
+  };
   bool open = false;
   for (int j = 0; j < m; j += kRedRows) {
-    float g[kRedRows][VEC];
-    uint32_t key[kRedRows + 1];
+    const Eight key = nk, val = nv;
+    Raw<EI, VEC> g[kRedRows];
 #pragma unroll
-    for (int q = 0; q < kRedRows; ++q) {
-      if (j + q < m) {
-        key[q] = tk[j + q];
-        load_vec<EI, VEC, true>(dout, int64_t(tv[j + q]) * dim + c, g[q]);
-      }
+    for (int q = 0; q < kRedRows; ++q)
+      if (j + q < m) fetch<true>(g[q], dout, int64_t(val.x[q]) * dim + c);
+    if (s0 + j + kRedRows < n) {
+      nk = load8(keys + s0 + j + kRedRows);  // (past the tile: its first key tells whether the last row goes on)
+      if (j + kRedRows < m) nv = load8(vals + s0 + j + kRedRows);
     }
-    const bool more = s0 + j + kRedRows < n;
-    key[kRedRows] = more ? tk[j + kRedRows] : 0u;
 #pragma unroll
     for (int q = 0; q < kRedRows; ++q) {
       if (j + q < m) {
+        float x[VEC];
+        unpack(g[q], x);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) acc[k] += g[q][k];
+        for (int k = 0; k < VEC; ++k) acc[k] += x[k];
         open = true;
-        if (s0 + j + q + 1 == n || key[q + 1] != key[q]) {  // the row's last entry
+        const uint32_t after = q + 1 < kRedRows ? key.x[(q + 1) % kRedRows] : nk.x[0];
+        if (s0 + j + q + 1 == n || after != key.x[q]) {  // the row's last entry
           if (from_prev) {
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) part_head[t * dim + c + k] = acc[k];
+            partial(part_head);
           } else if (uint64_t(u) < uint64_t(cap)) {
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) acc[k] *= scale;
-            store_vec<EO, VEC, true>(grads, u * dim + c, acc);
+            for (int k = 0; k < VEC; k += SV) {
+              float y[SV];
+#pragma unroll
+              for (int i = 0; i < SV; ++i) y[i] = acc[k + i] * scale;
+              store_vec<EO, SV, true>(grads, u * dim + c + k, y);
+            }
           }
           from_prev = false;
           open = false;
@@ -317,20 +332,17 @@ __global__ void __launch_bounds__(kRedThreads) grad_reduce_kernel(
       }
     }
   }
-  if (open) {  // the row goes on in the next tile: it began before this one, or here
-    float* part = from_prev ? part_head : part_tail;
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) part[t * dim + c + k] = acc[k];
-  }
+  if (open) partial(from_prev ? part_head : part_tail);  // the row goes on: it began before this tile, or here
 }
 
 // One warp per tile in which a row begins that goes on in the next tile:
 // the row's sum is the tile's tail plus the heads of the following tiles up to
 // the row's last.  Rows over more than kLongTiles tiles are added by the whole
-// block: warp w takes every 32nd tile, then the warps' sums in warp order.
-constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32, kLongTiles = 64;
+// block: warp w takes every 8th tile, then the warps' sums in warp order.
+// VEC columns a lane.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kLongTiles = 16;
 
-template <class EO>
+template <class EO, int VEC>
 __global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const uint32_t* __restrict__ keys,
                                                                  const int64_t* __restrict__ n_dev,
                                                                  const uint32_t* __restrict__ start,
@@ -339,30 +351,37 @@ __global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const uint32_t*
                                                                  int64_t cap, const float* __restrict__ part_head,
                                                                  const float* __restrict__ part_tail) {
   __shared__ uint32_t long_row[kJoinWarps];
-  __shared__ float sums[kJoinWarps][33];
+  __shared__ float sums[kJoinWarps][32 * VEC];
   const int64_t n = *n_dev;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t ntiles = (n + (int64_t(1) << chunk_log2) - 1) >> chunk_log2;
-  auto sum_tiles = [&](int64_t t, int64_t first, int64_t last, int64_t step, int c) {
-    float a = 0.f;
+  // heads of tiles first, first + step, ... up to last, added to a
+  auto sum_tiles = [&](float (&a)[VEC], int64_t first, int64_t last, int64_t step, int c) {
     int64_t v = first;
     for (; v + 7 * step <= last; v += 8 * step) {
-      float x[8];
+      float x[8][VEC];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) x[q] = part_head[(v + q * step) * dim + c];
+      for (int q = 0; q < 8; ++q) load_vec<F32, VEC, true>(part_head, (v + q * step) * dim + c, x[q]);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) a += x[q];
+      for (int q = 0; q < 8; ++q)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) a[k] += x[q][k];
     }
-    for (; v <= last; v += step) a += part_head[v * dim + c];
-    return a;
+    for (; v <= last; v += step) {
+      float x[VEC];
+      load_vec<F32, VEC, true>(part_head, v * dim + c, x);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) a[k] += x[k];
+    }
   };
   auto last_tile = [&](uint32_t u) {
     const int64_t v = int64_t(start[u + 1] - 1) >> chunk_log2;
     return v < ntiles ? v : ntiles - 1;
   };
-  auto put = [&](int64_t u, int c, float a) {
-    const float x[1] = {a * scale};
-    store_vec<EO, 1, false>(grads, u * dim + c, x);
+  auto put = [&](int64_t u, int c, float (&a)[VEC]) {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) a[k] *= scale;
+    store_vec<EO, VEC, false>(grads, u * dim + c, a);
   };
   for (int64_t t0 = int64_t(blockIdx.x) * kJoinWarps; t0 < ntiles; t0 += int64_t(gridDim.x) * kJoinWarps) {
     const int64_t t = t0 + warp;
@@ -375,8 +394,12 @@ __global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const uint32_t*
         const int64_t last = last_tile(u);
         is_long = last - t > kLongTiles;
         if (!is_long)
-          for (int c = lane; c < dim; c += 32)
-            put(u, c, part_tail[t * dim + c] + sum_tiles(t, t + 1, last, 1, c));
+          for (int c = lane * VEC; c < dim; c += 32 * VEC) {
+            float a[VEC];
+            load_vec<F32, VEC, true>(part_tail, t * dim + c, a);
+            sum_tiles(a, t + 1, last, 1, c);
+            put(u, c, a);
+          }
       }
     }
     if (lane == 0) long_row[warp] = is_long ? 1u : 0u;
@@ -386,13 +409,20 @@ __global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const uint32_t*
       const int64_t tl = t0 + w;
       const uint32_t u = before[tl + 1] - 1;
       const int64_t last = last_tile(u);
-      for (int c0 = 0; c0 < dim; c0 += 32) {
-        const int c = c0 + lane;
-        sums[warp][lane] = c < dim ? sum_tiles(tl, tl + 1 + warp, last, kJoinWarps, c) : 0.f;
+      for (int c0 = 0; c0 < dim; c0 += 32 * VEC) {
+        const int c = c0 + lane * VEC;
+        float a[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) a[k] = 0.f;
+        if (c < dim) sum_tiles(a, tl + 1 + warp, last, kJoinWarps, c);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) sums[warp][lane * VEC + k] = a[k];
         __syncthreads();
         if (warp == 0 && c < dim) {
-          float a = part_tail[tl * dim + c];
-          for (int q = 0; q < kJoinWarps; ++q) a += sums[q][lane];
+          load_vec<F32, VEC, true>(part_tail, tl * dim + c, a);
+          for (int q = 0; q < kJoinWarps; ++q)
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) a[k] += sums[q][lane * VEC + k];
           put(u, c, a);
         }
         __syncthreads();
@@ -525,8 +555,7 @@ extern "C" fs_status fs_emb_grad_rows(int64_t num_rows, int32_t dim, const int64
     launches += 1;
   }
   const int vec = ib == 4 ? 4 : 8;
-  // 16-byte loads of dout where rows and addresses allow them (bf16 rows to f32: 4 columns a lane, so that a
-  // lane's f32 store is 16 bytes too); element by element otherwise
+  // 16-byte loads of dout where rows and addresses allow them, element by element otherwise
   const bool wide = dim % vec == 0 && aligned(dout, 16) && aligned(row_grads, 16);
 #define FS_GRAD(EI, EO, V)                                                                          \
   do {                                                                                              \
@@ -535,17 +564,18 @@ extern "C" fs_status fs_emb_grad_rows(int64_t num_rows, int32_t dim, const int64
   } while (0)
   if (ib == 4 && ob == 4) FS_GRAD(F32, F32, 4);
   else if (ib == 4) FS_GRAD(F32, Bf16, 4);
-  else if (ob == 4) FS_GRAD(Bf16, F32, 4);
+  else if (ob == 4) FS_GRAD(Bf16, F32, 8);
   else FS_GRAD(Bf16, Bf16, 8);
 #undef FS_GRAD
-  const int64_t want = (L.tiles + kJoinWarps - 1) / kJoinWarps, most = int64_t(sm_count()) * 2;
-  const unsigned grid = unsigned(want < most ? want : most);
-  if (ob == 4)
-    grad_join_kernel<F32><<<grid, kJoinThreads, 0, st>>>(sk, G.W.pass.n_valid, G.start, G.before, L.chunk_log2, dim,
-                                                         scale, row_grads, cap_rows, G.part_head, G.part_tail);
-  else
-    grad_join_kernel<Bf16><<<grid, kJoinThreads, 0, st>>>(sk, G.W.pass.n_valid, G.start, G.before, L.chunk_log2, dim,
-                                                          scale, row_grads, cap_rows, G.part_head, G.part_tail);
+  const int64_t want = (L.tiles + kJoinWarps - 1) / kJoinWarps, most = int64_t(sm_count()) * 8;
+  auto join = [&](auto kern) {
+    kern<<<unsigned(want < most ? want : most), kJoinThreads, 0, st>>>(sk, G.W.pass.n_valid, G.start, G.before,
+                                                                       L.chunk_log2, dim, scale, row_grads, cap_rows,
+                                                                       G.part_head, G.part_tail);
+  };
+  const bool wide4 = dim % 4 == 0 && aligned(row_grads, 4 * ob);
+  if (ob == 4) wide4 ? join(grad_join_kernel<F32, 4>) : join(grad_join_kernel<F32, 1>);
+  else wide4 ? join(grad_join_kernel<Bf16, 4>) : join(grad_join_kernel<Bf16, 1>);
   count_launch(launches + 2);
   return launch_status();
 }
