@@ -65,13 +65,14 @@ __device__ __forceinline__ int query_tiles(const Tile& x, bool causal, int& firs
 constexpr int kPlanThreads = 1024, kBuckets = 1024;
 
 // Lists the tiles of all samples twice, by descending number of key tiles (for
-// queries) and of query tiles (for keys; only where by_key is given): a
+// queries; an entry stands for `span` neighbouring tiles, and its t counts such
+// groups) and of query tiles (for keys; only where by_key is given, span 1): a
 // counting sort over the tile counts by one block.  The order among equals
 // does not matter to any result.
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const int64_t* __restrict__ offsets, int64_t S, int64_t T,
                                                                  const int32_t* __restrict__ cand, bool causal,
-                                                                 int32_t* ntiles, Tile* by_query, Tile* by_key,
-                                                                 int32_t* err) {
+                                                                 int span, int32_t* ntiles, Tile* by_query,
+                                                                 Tile* by_key, int32_t* err) {
   __shared__ int32_t hist[2][kBuckets];
   __shared__ int32_t scan[32];
   for (int i = threadIdx.x; i < 2 * kBuckets; i += kPlanThreads) (&hist[0][0])[i] = 0;
@@ -91,9 +92,11 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const int64_t* 
         c = c < 0 ? 0 : L;
       }
       Tile x{int32_t(b), L, L - c, 0};
-      for (; x.t * kTile < L; ++x.t) {
+      for (; x.t * span * kTile < L; ++x.t) {
         int own, first;
-        const int nk = key_tiles(x, causal, own) + own;
+        Tile last = x;  // the entry's last tile has the most key tiles
+        last.t = min(x.t * span + span - 1, (L - 1) / kTile);
+        const int nk = key_tiles(last, causal, own) + own;
         f(x, bucket(nk), bucket(query_tiles(x, causal, first)));
       }
     }
@@ -150,8 +153,18 @@ struct AttnArgs {
 };
 
 // Wait of a whole warp for a barrier's phase, with a limit; sets the error word when it gives up.
+// The hand-overs between the warps of a block come every few hundred cycles, so it polls without
+// asking to sleep and looks at the clock only now and then.
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t phase, const AttnArgs& a) {
-  if (bulk::warp_wait(bar, phase & 1u, a.wait_ns)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t polls = 1;; ++polls) {
+    if (__all_sync(0xffffffffu, bulk::try_wait(bar, phase & 1u))) return true;
+    if ((polls & 1023u) == 0) {
+      const uint64_t now = bulk::global_ns();
+      if (t0 == 0) t0 = now;
+      if (__any_sync(0xffffffffu, now - t0 > a.wait_ns)) break;
+    }
+  }
   if ((threadIdx.x & 31) == 0) set_err(a.err, FS_ERR_TIMEOUT);
   return false;
 }
@@ -220,212 +233,295 @@ __device__ __forceinline__ unsigned char* align_smem(unsigned char* p) {
 
 // ------------------------------------------------------------- forward
 
-// Four warps hold one query row per thread; the fifth loads tiles and issues
-// the products.  x sits in 128 columns of tensor memory, p (bf16) over it, o
-// beside it: 256 columns, so two blocks share an SM and one block's products
-// run under the other's softmax.
-constexpr int kFwdThreads = 160;
-template <int DH> constexpr int fwd_stages() { return DH == 64 ? 2 : 1; }
-template <int DH> constexpr int fwd_smem() { return tile_bytes<DH>() * (1 + 2 * fwd_stages<DH>()) + 1024; }
+// One block per SM works through units: two query tiles that read the same
+// keys and values, so each loaded tile serves two products.  They are the same
+// positions of two query heads that share a key/value head, or, where the
+// number of sharing heads is odd, neighbouring tiles of one head.  A warpgroup
+// per query tile, one row a thread, does the softmax; one warp issues the
+// products, one the loads, which run ahead into the next unit.  Products of one
+// query tile run under the softmax of the other.  Tensor memory: x of each tile in 128
+// columns, p (bf16) over it, o beside them.
+// A softmax thread holds a row of 128 scores: the third warpgroup (loads,
+// products, two idle warps) gives registers to the other two.  384 threads are
+// launched with kFwdRegs each; 2 * 128 * 208 + 128 * 88 is that total.
+constexpr int kFwdThreads = 384, kFwdRegs = 168;
+template <int DH> constexpr int fwd_slots() { return DH == 64 ? 8 : 4; }
+template <int DH> constexpr int fwd_smem() { return tile_bytes<DH>() * (2 + fwd_slots<DH>()) + 1024; }
+
+struct FwdUnit {
+  Tile x;
+  int head[2], row[2];  // query head and tile index of each query tile
+  int nk[2], own[2];    // key tiles of the history, and whether its own tile follows
+  int kv_head, common, n;
+  bool by_head, both;
+
+  __device__ __forceinline__ FwdUnit(const Tile& tile, int part, const AttnArgs& a) : x(tile) {
+    const int group = a.heads / a.kv_heads;
+    by_head = group % 2 == 0;
+    if (by_head) {
+      head[0] = 2 * part, head[1] = 2 * part + 1;
+      row[0] = row[1] = x.t;
+    } else {
+      head[0] = head[1] = part;
+      row[0] = 2 * x.t, row[1] = 2 * x.t + 1;
+    }
+    kv_head = head[0] / group;
+    both = row[1] * kTile < x.L;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      Tile y = x;
+      y.t = row[i];
+      nk[i] = key_tiles(y, a.causal, own[i]);
+    }
+    if (!both) nk[1] = own[1] = 0;
+    common = max(nk[0], nk[1]);
+    n = common + own[0] + (by_head ? 0 : own[1]);
+  }
+  // The unit's j-th key tile, and whether query tile i meets it.
+  __device__ __forceinline__ int key_tile(int j) const {
+    return j < common ? j : ((j == common && own[0]) || by_head ? row[0] : row[1]);
+  }
+  __device__ __forceinline__ bool meets(int i, int j) const {
+    if (by_head) return true;
+    return i ? j < nk[1] || (own[1] && j == common + own[0]) : j < nk[0] || (own[0] && j == common);
+  }
+};
+
+// Units of this block: dealt out in rounds, back and forth, most work first.
+struct Deal {
+  int64_t units;
+  int64_t round = 0;
+  __device__ __forceinline__ int64_t next() {
+    const int64_t g = gridDim.x, b = blockIdx.x;
+    const int64_t u = round * g + ((round & 1) ? g - 1 - b : b);
+    ++round;
+    return u < units ? u : -1;
+  }
+};
 
 template <int DH>
-__global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_constant__ CUtensorMap mq,
+__global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_constant__ CUtensorMap mq,
                                                                   const __grid_constant__ CUtensorMap mk,
-                                                                  const __grid_constant__ CUtensorMap mv, AttnArgs a) {
-  constexpr int TB = tile_bytes<DH>(), NS = fwd_stages<DH>();
+                                                                  const __grid_constant__ CUtensorMap mv, AttnArgs a,
+                                                                  int parts) {
+  constexpr int TB = tile_bytes<DH>(), NS = fwd_slots<DH>();
   extern __shared__ unsigned char raw[];
-  __shared__ __align__(8) uint64_t bars[10];
+  __shared__ __align__(8) uint64_t bars[8 + 2 * NS];
   __shared__ uint32_t tmem_at;
-  const int head = int(blockIdx.x % unsigned(a.heads));
-  const int64_t at = blockIdx.x / unsigned(a.heads);
-  if (at >= *a.ntiles) return;
-  const Tile x = a.tiles[at];
-  const int kv_head = head / (a.heads / a.kv_heads);
-  int own;
-  const int nk = key_tiles(x, a.causal, own);
-  const int n = nk + own;
+  const int64_t units = int64_t(*a.ntiles) * parts;
+  if (int64_t(blockIdx.x) >= units) return;
   unsigned char* smem = align_smem(raw);
-  const uint32_t q_at = bulk::smem_addr(smem), k_at = q_at + TB, v_at = k_at + NS * TB;
+  const uint32_t q_at = bulk::smem_addr(smem), kv_at = q_at + 2 * TB;
   const uint32_t bar = bulk::smem_addr(bars);
-  const uint32_t q_full = bar, k_full = bar + 8, v_full = bar + 24, s_full = bar + 40, p_ready = bar + 48, o_done = bar + 56,
-                 drain = bar + 64, fin = bar + 72;
+  const uint32_t q_full = bar, q_free = bar + 8, s_full = bar + 16, p_ready = bar + 32, o_full = bar + 48, drain = bar + 56,
+                 full = bar + 64, free = bar + 64 + 8 * NS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 4) {
+  if (warp == 8) {
     if (lane == 0) {
-      tc::prefetch_map(&mq), tc::prefetch_map(&mk), tc::prefetch_map(&mv);
-      for (int i = 0; i < 10; ++i) bulk::mbar_init(bar + 8 * i, i == 6 ? 4 : 1);
+      for (int i = 0; i < 8 + 2 * NS; ++i) bulk::mbar_init(bar + 8 * i, i == 4 || i == 5 ? 4 : 1);
       bulk::fence_init();
     }
     __syncwarp();
-    tc::alloc(&tmem_at, 256);
+    tc::alloc(&tmem_at, 512);
     tc::fence_before();
   }
   __syncthreads();
   tc::fence_after();
-  const uint32_t s_at = tmem_at, o_at = tmem_at + 128;
-  auto key_tile = [&](int j) { return j < nk ? j : x.t; };
+  const uint32_t s_at = tmem_at, o_at = tmem_at + 256;  // of query tile 0; tile 1's follow
+  Deal deal{units};
+  bool ok = true;
 
-  if (warp == 4) {
-    int loaded_k = 0, loaded_v = 0;  // tiles asked for so far
-    auto load_k = [&](int j) {
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 9) {
+    // loads: the two query tiles of a unit, then its key and value tiles, in order, through NS slots
+    int64_t slot = 0;
+    for (int k = 0;; ++k) {
+      const int64_t u = deal.next();
+      if (u < 0) break;
+      const FwdUnit f(a.tiles[u / parts], int(u % parts), a);
+      if (k > 0 && !(ok = wait(q_free, k - 1, a))) break;
       if (lane == 0) {
-        bulk::arrive_expect_tx(k_full + 8 * (j % NS), TB);
-        load_tile<DH>(k_at + (j % NS) * TB, &mk, kv_head, x.begin + key_tile(j) * kTile, k_full + 8 * (j % NS));
+        bulk::arrive_expect_tx(q_full, f.both ? 2 * TB : TB);
+        load_tile<DH>(q_at, &mq, f.head[0], f.x.begin + f.row[0] * kTile, q_full);
+        if (f.both) load_tile<DH>(q_at + TB, &mq, f.head[1], f.x.begin + f.row[1] * kTile, q_full);
       }
-      loaded_k = j + 1;
-    };
-    auto load_v = [&](int j) {
-      if (lane == 0) {
-        bulk::arrive_expect_tx(v_full + 8 * (j % NS), TB);
-        load_tile<DH>(v_at + (j % NS) * TB, &mv, kv_head, x.begin + key_tile(j) * kTile, v_full + 8 * (j % NS));
-      }
-      loaded_v = j + 1;
-    };
-    if (lane == 0) {
-      bulk::arrive_expect_tx(q_full, TB);
-      load_tile<DH>(q_at, &mq, head, x.begin + x.t * kTile, q_full);
-    }
-    for (int j = 0; j < NS && j < n; ++j) {
-      load_k(j);
-      load_v(j);
-    }
-    bool ok = wait(q_full, 0, a) && wait(k_full, 0, a);
-    if (ok && lane == 0) {
-      mma_rows<DH>(s_at, q_at, k_at);
-      tc::commit(s_full);
-    }
-    for (int j = 0; ok && j < n; ++j) {
-      const int st = j % NS;
-      if (NS == 1 && j + 1 < n) {  // the key tile is free once its product is done
-        if (!(ok = wait(s_full, j, a))) break;
-        load_k(j + 1);
-      }
-      if (!(ok = wait(v_full + 8 * st, j / NS, a))) break;
-      const int valid = x.L - key_tile(j) * kTile;
-      if (valid < kTile) zero_rows<DH>(smem + TB * (1 + NS + st), valid);
-      if (!(ok = wait(p_ready, j, a))) break;
-      tc::fence_after();
-      if (lane == 0) {
-        mma_cols<DH>(o_at, s_at, s_at + 32, v_at + st * TB, j != 0);
-        tc::commit(j + 1 < n ? o_done : fin);
-      }
-      __syncwarp();
-      if (j + 1 < n) {
-        if (!(ok = wait(k_full + 8 * ((j + 1) % NS), (j + 1) / NS, a))) break;
+      for (int j = 0; ok && j < 2 * f.n; ++j, ++slot) {
+        const int s = int(slot % NS);
+        if (slot >= NS && !(ok = wait(free + 8 * s, uint32_t(slot / NS - 1), a))) break;
         if (lane == 0) {
-          // x overwrites p: the products execute in the order they are issued
-          mma_rows<DH>(s_at, q_at, k_at + ((j + 1) % NS) * TB);
-          tc::commit(s_full);
+          bulk::arrive_expect_tx(full + 8 * s, TB);
+          load_tile<DH>(kv_at + s * TB, j & 1 ? &mv : &mk, f.kv_head, f.x.begin + f.key_tile(j >> 1) * kTile,
+                        full + 8 * s);
+        }
+      }
+      if (!ok) break;
+    }
+    if (!ok)  // gave up: let what is in flight land
+      for (int64_t s = slot > NS ? slot - NS : 0; s < slot; ++s)
+        bulk::warp_wait(full + 8 * int(s % NS), uint32_t(s / NS) & 1u, a.wait_ns);
+    } else if (warp == 8) {
+    // products: at step j, o += p v of key tile j - 1 and x of key tile j, of query tile 0, then of 1
+    int64_t slot = 0;           // of the unit's first key tile
+    uint32_t done[2] = {0, 0};  // p's consumed
+    for (int k = 0; ok; ++k) {
+      const int64_t u = deal.next();
+      if (u < 0) break;
+      const FwdUnit f(a.tiles[u / parts], int(u % parts), a);
+      if (!(ok = wait(q_full, k, a))) break;
+      uint32_t acc[2] = {0, 0};
+      for (int j = 0; j <= f.n; ++j) {
+        const int64_t ks = slot + 2 * j, vs = ks - 1;  // slots of key tile j and value tile j - 1
+        const uint32_t k_tile = kv_at + uint32_t(ks % NS) * TB, v_tile = kv_at + uint32_t(vs % NS + NS) % NS * TB;
+        if (j > 0) {
+          if (!(ok = wait(full + 8 * int(vs % NS), uint32_t(vs / NS), a))) break;
+          const int valid = f.x.L - f.key_tile(j - 1) * kTile;
+          if (valid < kTile) zero_rows<DH>(smem + 2 * TB + int(vs % NS) * TB, valid);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (i == 1 && !f.both) continue;
+          if (j > 0 && f.meets(i, j - 1)) {
+            if (!(ok = wait(p_ready + 8 * i, done[i], a))) break;
+            ++done[i];
+            tc::fence_after();
+            if (lane == 0) mma_cols<DH>(o_at + i * DH, s_at + 128 * i, s_at + 128 * i + 32, v_tile, acc[i] != 0);
+            acc[i] = 1;
+          }
+          if (j < f.n && f.meets(i, j)) {
+            // x overwrites p: the products execute in the order they are issued
+            if (!(ok = wait(full + 8 * int(ks % NS), uint32_t(ks / NS), a))) break;
+            if (lane == 0) {
+              mma_rows<DH>(s_at + 128 * i, q_at + i * TB, k_tile);
+              tc::commit(s_full + 8 * i);
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          if (j > 0) tc::commit(free + 8 * int(vs % NS));
+          if (j < f.n) tc::commit(free + 8 * int(ks % NS));
+          if (j == f.n - 1) tc::commit(q_free);
+          if (j == f.n) tc::commit(o_full);
         }
         __syncwarp();
       }
-      if (j + NS < n) {
-        if (NS > 1) load_k(j + NS);  // (p_ready: the product that read this stage is done)
-        if (!(ok = wait(o_done, j, a))) break;
-        load_v(j + NS);
-      }
+      slot += 2 * f.n;
     }
-    if (!ok) {  // gave up: let what is in flight land
+    if (!ok) {
       if (lane == 0) tc::commit(drain);
       bulk::warp_wait(drain, 0, a.wait_ns);
-      bulk::warp_wait(q_full, 0, a.wait_ns);
-      for (int s = 0; s < NS; ++s) {
-        if (loaded_k > s) bulk::warp_wait(k_full + 8 * s, ((loaded_k - 1 - s) / NS) & 1, a.wait_ns);
-        if (loaded_v > s) bulk::warp_wait(v_full + 8 * s, ((loaded_v - 1 - s) / NS) & 1, a.wait_ns);
-      }
+    }
     }
   } else {
-    const int row = x.t * kTile + threadIdx.x;  // position inside the sample
-    const uint32_t lanes = uint32_t(warp * 32) << 16;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int i = warp >> 2;  // query tile of this warpgroup
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t x_at = s_at + 128 * i + lanes, acc_at = o_at + DH * i + lanes;
     const float c = a.scale * kLog2e;
-    float m = -INFINITY, l = 0.f;
-    bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      if (!(ok = wait(s_full, j, a))) break;
-      tc::fence_after();
-      float s[128];
+    uint32_t seen = 0;
+    for (int k = 0; ok; ++k) {
+      const int64_t u = deal.next();
+      if (u < 0) break;
+      const FwdUnit f(a.tiles[u / parts], int(u % parts), a);
+      const int tile = i ? f.row[1] : f.row[0];
+      const int row = tile * kTile + int(threadIdx.x & 127);  // position inside the sample
+      float m = -INFINITY, l = 0.f;
+      bool first = true;
+      for (int j = 0; j < f.n; ++j) {
+        if ((i == 1 && !f.both) || !f.meets(i, j)) continue;
+        if (!(ok = wait(s_full + 8 * i, seen, a))) break;
+        ++seen;
+        tc::fence_after();
+        float s[128];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) tc::ld32(s_at + lanes + 32 * b, s + 32 * b);
-      tc::wait_ld();
+        for (int b = 0; b < 4; ++b) tc::ld32(x_at + 32 * b, s + 32 * b);
+        tc::wait_ld();
 #pragma unroll
-      for (int b = 0; b < 4; ++b) tc::tie32(s + 32 * b);
-      const int k0 = key_tile(j) * kTile;
-      if (k0 + kTile > x.uih || (a.causal && k0 + kTile > x.t * kTile)) {
-        const int lim = (a.causal ? min(x.uih, row + 1) : x.uih) - k0, self = row - k0;
+        for (int b = 0; b < 4; ++b) tc::tie32(s + 32 * b);
+        const int k0 = f.key_tile(j) * kTile;
+        if (k0 + kTile > f.x.uih || (a.causal && k0 + kTile > tile * kTile)) {
+          const int lim = (a.causal ? min(f.x.uih, row + 1) : f.x.uih) - k0, self = row - k0;
 #pragma unroll
-        for (int i = 0; i < 128; ++i) s[i] = (i < lim || i == self) ? s[i] : -INFINITY;
-      }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
+          for (int q = 0; q < 128; ++q) s[q] = (q < lim || q == self) ? s[q] : -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int i = 4; i < 128; i += 8) {
+        for (int q = 4; q < 124; q += 8) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], i + 4 + q < 128 ? fmaxf(s[i + q], s[i + 4 + q]) : s[i + q]);
-      }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      if (j == 0) {
-        m = top;
-      } else {
-        // the sums keep an older maximum until a row's has grown by 2^8: p stays
-        // below 2^8, its rounding relative, and o is rescaled only then
-        const bool grow = (top - m) * c > 8.f;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float mn = grow ? top : m, f = tc::ex2((m - mn) * c);
-          m = mn;
-          l *= f;
+          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], fmaxf(s[q + e], s[q + 4 + e]));
+        }
 #pragma unroll
-          for (int b = 0; b < DH / 32; ++b) {
-            float o[32];
-            tc::ld32(o_at + lanes + 32 * b, o);
-            tc::wait_ld();
-            tc::tie32(o);
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[124 + e]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (first) {
+          m = top;
+          first = false;
+        } else {
+          // the sums keep an older maximum until a row's has grown by 2^8: p stays
+          // below 2^8, its rounding relative, and o is rescaled only then
+          const bool grow = (top - m) * c > 8.f;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mn = grow ? top : m, g = tc::ex2((m - mn) * c);
+            m = mn;
+            l *= g;
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) tc::mul2(o + i, f, f);
-            tc::st32(o_at + lanes + 32 * b, reinterpret_cast<const uint32_t*>(o));
+            for (int b = 0; b < DH / 32; ++b) {
+              float o[32];
+              tc::ld32(acc_at + 32 * b, o);
+              tc::wait_ld();
+              tc::tie32(o);
+#pragma unroll
+              for (int q = 0; q < 32; q += 2) tc::mul2(o + q, g, g);
+              tc::st32(acc_at + 32 * b, reinterpret_cast<const uint32_t*>(o));
+            }
           }
         }
-      }
-      const float mc = -m * c;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      uint32_t p[64];
+        const float mc = -m * c;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t p[64];
 #pragma unroll
-      for (int i = 0; i < 128; i += 4) {
-        tc::fma2(s + i, c, c, mc, mc);
-        tc::fma2(s + i + 2, c, c, mc, mc);
+        for (int q = 0; q < 128; q += 4) {
+          tc::fma2(s + q, c, c, mc, mc);
+          tc::fma2(s + q + 2, c, c, mc, mc);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) s[i + q] = tc::ex2(s[i + q]);
-        tc::add2(sum, s[i], s[i + 1]);
-        tc::add2(sum + 2, s[i + 2], s[i + 3]);
-        p[i / 2] = tc::pack2(s[i], s[i + 1]);
-        p[i / 2 + 1] = tc::pack2(s[i + 2], s[i + 3]);
-        if (i == 60) tc::st32(s_at + lanes, p);
+          for (int e = 0; e < 4; ++e) s[q + e] = tc::ex2(s[q + e]);
+          tc::add2(sum, s[q], s[q + 1]);
+          tc::add2(sum + 2, s[q + 2], s[q + 3]);
+          p[q / 2] = tc::pack2(s[q], s[q + 1]);
+          p[q / 2 + 1] = tc::pack2(s[q + 2], s[q + 3]);
+          if (q == 60) tc::st32(x_at, p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tc::st32(x_at + 32, p + 32);
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::arrive(p_ready + 8 * i);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tc::st32(s_at + lanes + 32, p + 32);
-      tc::wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::arrive(p_ready);
-    }
-    if (ok && wait(fin, 0, a)) {
+      if (!ok || !(ok = wait(o_full, k, a))) break;
       tc::fence_after();
-      const int64_t pos = int64_t(x.begin) + row;
+      if (i == 1 && !f.both) continue;
+      const int64_t pos = int64_t(f.x.begin) + row;
+      const int head = i ? f.head[1] : f.head[0];
       const float inv = 1.f / l;
 #pragma unroll
       for (int b = 0; b < DH / 32; ++b) {
         float o[32];
-        tc::ld32(o_at + lanes + 32 * b, o);
+        tc::ld32(acc_at + 32 * b, o);
         tc::wait_ld();
         tc::tie32(o);
-        if (row < x.L) store32(a.o + (pos * a.heads + head) * DH + 32 * b, o, inv);
+        if (row < f.x.L) store32(a.o + (pos * a.heads + head) * DH + 32 * b, o, inv);
       }
-      if (row < x.L) a.lse[int64_t(head) * a.T + pos] = (m * c + log2f(l)) * (1.f / kLog2e);
+      if (row < f.x.L) a.lse[int64_t(head) * a.T + pos] = (m * c + log2f(l)) * (1.f / kLog2e);
       tc::fence_before();
     }
   }
   __syncthreads();
-  if (warp == 4) {
+  if (warp == 8) {
     tc::fence_after();
-    tc::dealloc(tmem_at, 256);
+    tc::dealloc(tmem_at, 512);
   }
 }
 
@@ -946,14 +1042,20 @@ void take_attn(int64_t T, int64_t S, int32_t Hq, Ws& ws, AttnWs& W) {
   W.delta = ws.template take<float>(size_t(Hq) * size_t(T));
 }
 
-// Allows a kernel its shared memory, once per device (`done` holds a bit for each).
+// Allows a kernel its shared memory, once per device (`done` holds a bit for each).  A kernel
+// that moves registers between its warps (regs > 0) must have been built with that many a
+// thread: with fewer, the warps that ask for more would wait for ever.
 template <class K>
-void raise_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
+bool prepare_kernel(K kern, int bytes, int regs, std::atomic<uint64_t>& done) {
   int dev = 0;
-  cudaGetDevice(&dev);
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
   const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
-  if (bit && (done.load(std::memory_order_relaxed) & bit)) return;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess) done.fetch_or(bit);
+  if (bit && (done.load(std::memory_order_relaxed) & bit)) return true;
+  cudaFuncAttributes f;
+  if (cudaFuncGetAttributes(&f, kern) != cudaSuccess || f.numRegs < regs) return false;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  done.fetch_or(bit);
+  return true;
 }
 
 std::atomic<uint64_t> g_fwd_ready[2], g_bwd_ready[2][2];
@@ -1001,14 +1103,18 @@ extern "C" fs_status fs_jagged_attn(const void* q, int64_t q_stride, const void*
   a.heads = heads, a.kv_heads = kv_heads, a.T = T, a.causal = causal != 0, a.scale = scale;
   a.o = static_cast<__nv_bfloat16*>(out), a.lse = lse, a.err = err;
   a.wait_ns = uint64_t(spin_limit()) * 256u;
-  attn_plan_kernel<<<1, kPlanThreads, 0, st>>>(offsets, S, T, cand_len, a.causal, W.ntiles, W.by_query, nullptr, err);
-  const unsigned grid = unsigned(most_tiles(T, S) * heads);
+  const bool by_head = heads / kv_heads % 2 == 0;  // two heads of one tile share a block, else two tiles of one head
+  const int parts = by_head ? heads / 2 : heads;
+  attn_plan_kernel<<<1, kPlanThreads, 0, st>>>(offsets, S, T, cand_len, a.causal, by_head ? 1 : 2, W.ntiles, W.by_query,
+                                               nullptr, err);
+  const int64_t units = most_tiles(T, S) * parts;
+  const unsigned grid = unsigned(units < sm_count() ? units : sm_count());
   if (head_dim == 64) {
-    raise_smem(attn_fwd_kernel<64>, fwd_smem<64>(), g_fwd_ready[0]);
-    attn_fwd_kernel<64><<<grid, kFwdThreads, fwd_smem<64>(), st>>>(mq, mk, mv, a);
+    if (!prepare_kernel(attn_fwd_kernel<64>, fwd_smem<64>(), kFwdRegs, g_fwd_ready[0])) return FS_ERR_CUDA;
+    attn_fwd_kernel<64><<<grid, kFwdThreads, fwd_smem<64>(), st>>>(mq, mk, mv, a, parts);
   } else {
-    raise_smem(attn_fwd_kernel<128>, fwd_smem<128>(), g_fwd_ready[1]);
-    attn_fwd_kernel<128><<<grid, kFwdThreads, fwd_smem<128>(), st>>>(mq, mk, mv, a);
+    if (!prepare_kernel(attn_fwd_kernel<128>, fwd_smem<128>(), kFwdRegs, g_fwd_ready[1])) return FS_ERR_CUDA;
+    attn_fwd_kernel<128><<<grid, kFwdThreads, fwd_smem<128>(), st>>>(mq, mk, mv, a, parts);
   }
   count_launch(2);
   return launch_status();
@@ -1051,18 +1157,18 @@ extern "C" fs_status fs_jagged_attn_backward(const void* q, int64_t q_stride, co
   a.dq = static_cast<__nv_bfloat16*>(dq), a.dk = static_cast<__nv_bfloat16*>(dk), a.dv = static_cast<__nv_bfloat16*>(dv);
   a.dq_stride = dq_stride, a.dk_stride = dk_stride, a.dv_stride = dv_stride;
   a.wait_ns = uint64_t(spin_limit()) * 256u;
-  attn_plan_kernel<<<1, kPlanThreads, 0, st>>>(offsets, S, T, cand_len, a.causal, W.ntiles, W.by_query, W.by_key, err);
+  attn_plan_kernel<<<1, kPlanThreads, 0, st>>>(offsets, S, T, cand_len, a.causal, 1, W.ntiles, W.by_query, W.by_key, err);
   const unsigned gq = unsigned(most_tiles(T, S) * heads), gk = unsigned(most_tiles(T, S) * kv_heads);
   AttnArgs b = a;
   a.tiles = W.by_query, b.tiles = W.by_key;
   if (head_dim == 64) {
-    raise_smem(attn_dq_kernel<64>, bwd_smem<64>(), g_bwd_ready[0][0]);
-    raise_smem(attn_dkv_kernel<64>, bwd_smem<64>(), g_bwd_ready[0][1]);
+    if (!prepare_kernel(attn_dq_kernel<64>, bwd_smem<64>(), 0, g_bwd_ready[0][0])) return FS_ERR_CUDA;
+    if (!prepare_kernel(attn_dkv_kernel<64>, bwd_smem<64>(), 0, g_bwd_ready[0][1])) return FS_ERR_CUDA;
     attn_dq_kernel<64><<<gq, kBwdThreads, bwd_smem<64>(), st>>>(mq, mk, mv, mdo, a);
     attn_dkv_kernel<64><<<gk, kBwdThreads, bwd_smem<64>(), st>>>(mq, mk, mv, mdo, b);
   } else {
-    raise_smem(attn_dq_kernel<128>, bwd_smem<128>(), g_bwd_ready[1][0]);
-    raise_smem(attn_dkv_kernel<128>, bwd_smem<128>(), g_bwd_ready[1][1]);
+    if (!prepare_kernel(attn_dq_kernel<128>, bwd_smem<128>(), 0, g_bwd_ready[1][0])) return FS_ERR_CUDA;
+    if (!prepare_kernel(attn_dkv_kernel<128>, bwd_smem<128>(), 0, g_bwd_ready[1][1])) return FS_ERR_CUDA;
     attn_dq_kernel<128><<<gq, kBwdThreads, bwd_smem<128>(), st>>>(mq, mk, mv, mdo, a);
     attn_dkv_kernel<128><<<gk, kBwdThreads, bwd_smem<128>(), st>>>(mq, mk, mv, mdo, b);
   }
