@@ -190,25 +190,42 @@ __device__ __forceinline__ void zero_rows(unsigned char* tile, int from) {
   __syncwarp();
 }
 
-// D[128 x 128] = A B^T over DH columns, both tiles K-major (one thread).
+// D[128 x 128] = A B^T over DH columns, both tiles K-major.  Called by a whole warp; lane 0 issues.
 template <int DH>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b) {
   constexpr uint32_t id = tc::idesc(kTile, kTile, false);
+  d = tc::uni(d);
+  const uint32_t da = tc::uni(tc::desc_k(a)), db = tc::uni(tc::desc_k(b));
+  if ((threadIdx.x & 31) == 0) {
+    tc::mma_ss<true>(d, tc::at(da, 0), tc::at(db, 0), id, false);
 #pragma unroll
-  for (int k = 0; k < DH / 16; ++k) {
-    const uint32_t off = (k / 4) * kBox + (k % 4) * 32;
-    tc::mma_ss(d, tc::desc_k(a + off), tc::desc_k(b + off), id, k != 0);
+    for (int k = 1; k < DH / 16; ++k) {
+      const uint32_t off = (k / 4) * kBox + (k % 4) * 32;
+      tc::mma_ss<false>(d, tc::at(da, off), tc::at(db, off), id, true);
+    }
   }
 }
 
 // D[128 x DH] (+)= A B, A [128 x 128] bf16 in tensor memory, its first 64 columns at a0, the
-// others at a1, B a tile of 128 rows (one thread).
+// others at a1, B a tile of 128 rows.  Called by a whole warp; lane 0 issues.
 template <int DH>
 __device__ __forceinline__ void mma_cols(uint32_t d, uint32_t a0, uint32_t a1, uint32_t b, bool acc) {
   constexpr uint32_t id = tc::idesc(kTile, DH, true);
+  d = tc::uni(d), a0 = tc::uni(a0), a1 = tc::uni(a1);
+  const uint32_t db = tc::uni(tc::desc_mn(b, kBox));
+  const bool on = tc::uni(uint32_t(acc)) != 0;
+  if ((threadIdx.x & 31) == 0) {
+    tc::mma_ts<true>(d, a0, tc::at(db, 0), id, on);
 #pragma unroll
-  for (int k = 0; k < kTile / 16; ++k)
-    tc::mma_ts(d, (k < 4 ? a0 + 8 * k : a1 + 8 * (k - 4)), tc::desc_mn(b + k * 2048, kBox), id, acc || k != 0);
+    for (int k = 1; k < kTile / 16; ++k)
+      tc::mma_ts<false>(d, (k < 4 ? a0 + 8 * k : a1 + 8 * (k - 4)), tc::at(db, k * 2048), id, true);
+  }
+}
+
+// Commit by the lane that issues the products.
+__device__ __forceinline__ void commit(uint32_t bar) {
+  bar = tc::uni(bar);
+  if ((threadIdx.x & 31) == 0) tc::commit(bar);
 }
 
 // 32 fp32 columns, scaled, as bf16 to 64 contiguous bytes.
@@ -315,7 +332,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
   const uint32_t bar = bulk::smem_addr(bars);
   const uint32_t q_full = bar, q_free = bar + 8, s_full = bar + 16, p_ready = bar + 32, o_full = bar + 48, drain = bar + 56,
                  full = bar + 64, free = bar + 64 + 8 * NS;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = int(tc::uni(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (warp == 8) {
     if (lane == 0) {
       for (int i = 0; i < 8 + 2 * NS; ++i) bulk::mbar_init(bar + 8 * i, i == 4 || i == 5 ? 4 : 1);
@@ -385,27 +402,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
             if (!(ok = wait(p_ready + 8 * i, done[i], a))) break;
             ++done[i];
             tc::fence_after();
-            if (lane == 0) mma_cols<DH>(o_at + i * DH, s_at + 128 * i, s_at + 128 * i + 32, v_tile, acc[i] != 0);
+            mma_cols<DH>(o_at + i * DH, s_at + 128 * i, s_at + 128 * i + 32, v_tile, acc[i] != 0);
             acc[i] = 1;
           }
           if (j < f.n && f.meets(i, j)) {
             // x overwrites p: the products execute in the order they are issued
             if (!(ok = wait(full + 8 * int(ks % NS), uint32_t(ks / NS), a))) break;
-            if (lane == 0) {
-              mma_rows<DH>(s_at + 128 * i, q_at + i * TB, k_tile);
-              tc::commit(s_full + 8 * i);
-            }
+            mma_rows<DH>(s_at + 128 * i, q_at + i * TB, k_tile);
+            commit(s_full + 8 * i);
           }
-          __syncwarp();
         }
         if (!ok) break;
-        if (lane == 0) {
-          if (j > 0) tc::commit(free + 8 * int(vs % NS));
-          if (j < f.n) tc::commit(free + 8 * int(ks % NS));
-          if (j == f.n - 1) tc::commit(q_free);
-          if (j == f.n) tc::commit(o_full);
-        }
-        __syncwarp();
+        if (j > 0) commit(free + 8 * int(vs % NS));
+        if (j < f.n) commit(free + 8 * int(ks % NS));
+        if (j == f.n - 1) commit(q_free);
+        if (j == f.n) commit(o_full);
       }
       slot += 2 * f.n;
     }
@@ -557,7 +568,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
   const uint32_t bar = bulk::smem_addr(bars);
   const uint32_t q_full = bar, k_full = bar + 8, v_full = bar + 24, s_full = bar + 40, dp_full = bar + 48,
                  s_read = bar + 56, ds_ready = bar + 64, dq_done = bar + 72, drain = bar + 80, fin = bar + 88;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = int(tc::uni(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (warp == 8) {
     if (lane == 0) {
       tc::prefetch_map(&mq), tc::prefetch_map(&mk), tc::prefetch_map(&mv), tc::prefetch_map(&mdo);
@@ -605,39 +616,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
       load_v(j);
     }
     bool ok = wait(q_full, 0, a) && key_ready(0) && wait(v_full, 0, a);
-    if (ok && lane == 0) {
+    if (ok) {
       mma_rows<DH>(s_at, q_at, k_at);
-      tc::commit(s_full);
+      commit(s_full);
       mma_rows<DH>(dp_at, do_at, v_at);
-      tc::commit(dp_full);
+      commit(dp_full);
     }
-    __syncwarp();
     for (int j = 0; ok && j < n; ++j) {
       const int st = j & 1, nx = st ^ 1;
       if (j + 1 < n) {
         if (!(ok = key_ready(j + 1) && wait(s_read, j, a))) break;
         tc::fence_after();
-        if (lane == 0) {
-          mma_rows<DH>(s_at, q_at, k_at + nx * TB);
-          tc::commit(s_full);
-        }
-        __syncwarp();
+        mma_rows<DH>(s_at, q_at, k_at + nx * TB);
+        commit(s_full);
       }
       if (!(ok = wait(ds_ready, j, a))) break;
       tc::fence_after();
-      if (lane == 0) {
-        mma_cols<DH>(dq_at, dp_at, dp_at + 64, k_at + st * TB, j != 0);
-        tc::commit(j + 1 < n ? dq_done : fin);
-      }
-      __syncwarp();
+      mma_cols<DH>(dq_at, dp_at, dp_at + 64, k_at + st * TB, j != 0);
+      commit(j + 1 < n ? dq_done : fin);
       if (j + 1 < n) {
         if (!(ok = wait(v_full + 8 * nx, (j + 1) >> 1, a))) break;
-        if (lane == 0) {
-          // do v^T overwrites ds: the products execute in the order they are issued
-          mma_rows<DH>(dp_at, do_at, v_at + nx * TB);
-          tc::commit(dp_full);
-        }
-        __syncwarp();
+        // do v^T overwrites ds: the products execute in the order they are issued
+        mma_rows<DH>(dp_at, do_at, v_at + nx * TB);
+        commit(dp_full);
       }
       if (j + 2 < n) {
         load_v(j + 2);  // (ds_ready: the product that read this stage is done)
@@ -781,7 +782,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
   const uint32_t bar = bulk::smem_addr(bars);
   const uint32_t k_full = bar, q_full = bar + 8, s_full = bar + 24, dp_full = bar + 32, p_ready = bar + 40,
                  ds_ready = bar + 48, done = bar + 56, drain = bar + 64, fin = bar + 72;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = int(tc::uni(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (warp == 8) {
     if (lane == 0) {
       tc::prefetch_map(&mq), tc::prefetch_map(&mk), tc::prefetch_map(&mv), tc::prefetch_map(&mdo);
@@ -826,37 +827,30 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
     }
     for (int j = 0; j < 2 && j < n; ++j) load_q(j);
     bool ok = wait(k_full, 0, a) && query_ready(0);
-    if (ok && lane == 0) {
+    if (ok) {
       mma_rows<DH>(s_at, k_at, q_at);
-      tc::commit(s_full);
+      commit(s_full);
       mma_rows<DH>(dp_at, v_at, q_at + TB);
-      tc::commit(dp_full);
+      commit(dp_full);
     }
-    __syncwarp();
     for (int j = 0; ok && j < n; ++j) {
       const uint32_t cur = q_at + (j & 1) * 2 * TB, nxt = q_at + ((j + 1) & 1) * 2 * TB;
       if (j + 1 < n && !(ok = query_ready(j + 1))) break;
       if (!(ok = wait(p_ready, j, a))) break;
       tc::fence_after();
-      if (lane == 0) {
-        mma_cols<DH>(dv_at, s_at, s_at + 64, cur + TB, j != 0);
-        if (j + 1 < n) {  // x^T overwrites p^T: the products execute in the order they are issued
-          mma_rows<DH>(s_at, k_at, nxt);
-          tc::commit(s_full);
-        }
+      mma_cols<DH>(dv_at, s_at, s_at + 64, cur + TB, j != 0);
+      if (j + 1 < n) {  // x^T overwrites p^T: the products execute in the order they are issued
+        mma_rows<DH>(s_at, k_at, nxt);
+        commit(s_full);
       }
-      __syncwarp();
       if (!(ok = wait(ds_ready, j, a))) break;
       tc::fence_after();
-      if (lane == 0) {
-        mma_cols<DH>(dk_at, dp_at, dp_at + 64, cur, j != 0);
-        tc::commit(j + 1 < n ? done : fin);
-        if (j + 1 < n) {
-          mma_rows<DH>(dp_at, v_at, nxt + TB);
-          tc::commit(dp_full);
-        }
+      mma_cols<DH>(dk_at, dp_at, dp_at + 64, cur, j != 0);
+      commit(j + 1 < n ? done : fin);
+      if (j + 1 < n) {
+        mma_rows<DH>(dp_at, v_at, nxt + TB);
+        commit(dp_full);
       }
-      __syncwarp();
       if (j + 2 < n) {
         if (!(ok = wait(done, j, a))) break;
         load_q(j + 2);

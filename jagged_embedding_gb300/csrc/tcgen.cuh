@@ -20,19 +20,28 @@ namespace tc {
 
 // Shared-memory matrix descriptor, 128-byte swizzle: start address, leading
 // and stride byte offsets in units of 16 bytes, descriptor version 1 (bit 46),
-// swizzle mode 2 in bits 61..63.
-__device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t((lbo >> 4) & 0x3FFFu) << 16) |
-         (uint64_t((sbo >> 4) & 0x3FFFu) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+// swizzle mode 2 in bits 61..63.  The high word is the same for every operand
+// here (8-row groups 1024 bytes apart); the low word moves with the address.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+// K-major operand (the leading offset is unused with a swizzle): 16 columns of
+// K are 32 bytes further on.
+__device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+
+// MN-major operand: groups of 8 K-rows are the 1024-byte groups, the next 64
+// columns of N lie `box` bytes away; 16 rows of K are 2048 bytes further on.
+__device__ __forceinline__ uint32_t desc_mn(uint32_t addr, uint32_t box) { return (addr >> 4) | ((box >> 4) << 16); }
+
+// The descriptor `bytes` further on (shared memory ends below the address field's limit: no carry).
+__device__ __forceinline__ uint64_t at(uint32_t low, uint32_t bytes) {
+  return (uint64_t(kDescHigh) << 32) | (low + (bytes >> 4));
 }
 
-// K-major operand: 8-row groups 1024 bytes apart (the leading offset is unused
-// with a swizzle); 16 columns of K are 32 bytes further on.
-__device__ __forceinline__ uint64_t desc_k(uint32_t addr) { return desc(addr, 16, 1024); }
-
-// MN-major operand: groups of 8 K-rows 1024 bytes apart, the next 64 columns
-// of N `box` bytes away; 16 rows of K are 2048 bytes further on.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t box) { return desc(addr, box, 1024); }
+// The same value in every lane, known to the compiler as such.  A product's
+// operands go through uniform registers: an address that differs per thread, as far as the
+// compiler can tell, costs a round trip per product (measured: 90 to 200 cycles a product
+// of 128 x 128 x 16 instead of the 64 it takes to execute).
+__device__ __forceinline__ uint32_t uni(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // Instruction descriptor of kind::f16: fp32 accumulators, bf16 operands, A
 // K-major (or in tensor memory), B K-major or MN-major.
@@ -98,21 +107,37 @@ __device__ __forceinline__ void st32(uint32_t addr, const uint32_t* u) {
 // ------------------------------------------------------------- MMA (one thread)
 
 // D (tensor memory, fp32) = A * B + (acc ? D : 0), both operands in shared memory.
+template <bool FIRST>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(uint32_t(acc))
-      : "memory");
+  if constexpr (FIRST)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(uint32_t(acc))
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.eq.u32 p, 0, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(id)
+        : "memory");
 }
 
 // The same with A in tensor memory (two bf16 of K per 32-bit column).
+template <bool FIRST>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(uint32_t(acc))
-      : "memory");
+  if constexpr (FIRST)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(uint32_t(acc))
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.eq.u32 p, 0, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(id)
+        : "memory");
 }
 
 // One arrival on `bar` once every tcgen05 operation this thread issued before has completed.
