@@ -10,9 +10,16 @@
 //
 // A sample is cut into tiles of 128 positions, the same for queries and keys.
 // A planning kernel lists the tiles of all samples, those with the most work
-// first, so that blocks taken in order leave no long tail.  One block per tile
-// and head then walks the tiles that its rows (or, for dk and dv, its keys)
-// meet: whole tiles that nothing of which is visible are never loaded.
+// first; one block per SM then takes units (a tile and a head) from the list as
+// it gets free, and walks the tiles that the unit's rows (or, for dk and dv,
+// its keys) meet: tiles nothing of which is visible are never loaded.
+//
+// Roles inside a block: one warp takes units and loads tiles by TMA through a
+// ring of shared-memory slots, running ahead into the next unit; one thread
+// issues the products; two warpgroups do the elementwise part
+// with the scores in tensor memory.  They meet at mbarriers only.  Every wait has a
+// limit, after which the error word is set, copies and products in flight are
+// waited for and the block ends.
 //
 // The backward pass is two kernels: one block per query tile for dq, one per
 // key tile for dk and dv, each summing in its own accumulators, so every sum
@@ -22,6 +29,7 @@
 
 #include <atomic>
 #include <mutex>
+#include <utility>
 
 #include "fs_common.cuh"
 #include "tcgen.cuh"
@@ -62,47 +70,80 @@ __device__ __forceinline__ int query_tiles(const Tile& x, bool causal, int& firs
   return all - first;
 }
 
-constexpr int kPlanThreads = 1024, kBuckets = 1024;
+constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32, kBuckets = 1024;
+
+struct Plan {
+  int32_t ntiles;
+  int32_t next[2];  // units handed out beyond the first of each block: queries, keys
+};
 
 // Lists the tiles of all samples twice, by descending number of key tiles (for
 // queries; an entry stands for `span` neighbouring tiles, and its t counts such
 // groups) and of query tiles (for keys; only where by_key is given, span 1): a
 // counting sort over the tile counts by one block.  The order among equals
-// does not matter to any result.
+// does not matter to any result.  A warp takes up to 32 samples at a time and
+// spreads their tiles over its lanes.
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const int64_t* __restrict__ offsets, int64_t S, int64_t T,
                                                                  const int32_t* __restrict__ cand, bool causal,
-                                                                 int span, int32_t* ntiles, Tile* by_query,
-                                                                 Tile* by_key, int32_t* err) {
+                                                                 int span, Plan* plan, Tile* by_query, Tile* by_key,
+                                                                 int32_t* err) {
   __shared__ int32_t hist[2][kBuckets];
   __shared__ int32_t scan[32];
+  asm volatile("griddepcontrol.launch_dependents;");
   for (int i = threadIdx.x; i < 2 * kBuckets; i += kPlanThreads) (&hist[0][0])[i] = 0;
+  if (threadIdx.x < 2) plan->next[threadIdx.x] = 0;
   __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = span * kTile;
+  const int64_t share = (S + kPlanWarps - 1) / kPlanWarps;
+  const int group = share < 32 ? int(share) : 32;  // samples a warp takes at a time
   auto bucket = [](int cost) { return kBuckets - min(cost, kBuckets); };  // most work first
   auto each = [&](bool report, auto f) {
-    for (int64_t s = threadIdx.x; s < S; s += kPlanThreads) {
-      const int64_t b = offsets[s], e = offsets[s + 1];
-      if (b < 0 || e < b || e > T) {
-        if (report) set_err(err, FS_ERR_BAD_OFFSETS);
-        continue;
+    for (int64_t s0 = int64_t(warp) * group; s0 < S; s0 += int64_t(kPlanWarps) * group) {
+      int32_t begin = 0, L = 0, c = 0;
+      if (lane < group && s0 + lane < S) {
+        const int64_t b = offsets[s0 + lane], e = offsets[s0 + lane + 1];
+        if (b < 0 || e < b || e > T) {
+          if (report) set_err(err, FS_ERR_BAD_OFFSETS);
+        } else {
+          begin = int32_t(b);
+          L = int32_t(e - b);
+          c = cand ? cand[s0 + lane] : 0;
+          if (c < 0 || c > L) {
+            if (report) set_err(err, FS_ERR_INVALID_ARG);
+            c = c < 0 ? 0 : L;
+          }
+        }
       }
-      const int32_t L = int32_t(e - b);
-      int32_t c = cand ? cand[s] : 0;
-      if (c < 0 || c > L) {
-        if (report) set_err(err, FS_ERR_INVALID_ARG);
-        c = c < 0 ? 0 : L;
+      const int32_t mine = (L + rows - 1) / rows;
+      int32_t upto = mine;  // inclusive over the lanes
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
       }
-      Tile x{int32_t(b), L, L - c, 0};
-      for (; x.t * span * kTile < L; ++x.t) {
-        int own, first;
-        Tile last = x;  // the entry's last tile has the most key tiles
-        last.t = min(x.t * span + span - 1, (L - 1) / kTile);
-        const int nk = key_tiles(last, causal, own) + own;
-        f(x, bucket(nk), bucket(query_tiles(x, causal, first)));
+      const int32_t all = __shfl_sync(0xffffffffu, upto, 31);
+      for (int32_t i0 = 0; i0 < all; i0 += 32) {
+        const int32_t i = i0 + lane;
+        int who = 0;  // lanes whose tiles end at or before i
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+          if (__shfl_sync(0xffffffffu, upto, (who + o - 1) & 31) <= i) who += o;
+        who &= 31;
+        Tile x{__shfl_sync(0xffffffffu, begin, who), __shfl_sync(0xffffffffu, L, who), 0, 0};
+        x.uih = x.L - __shfl_sync(0xffffffffu, c, who);
+        x.t = i - (__shfl_sync(0xffffffffu, upto, who) - __shfl_sync(0xffffffffu, mine, who));
+        if (i < all) {
+          int own, first;
+          Tile last = x;  // the entry's last tile has the most key tiles
+          last.t = min(x.t * span + span - 1, (x.L - 1) / kTile);
+          const int nk = key_tiles(last, causal, own) + own;
+          f(x, bucket(nk), bucket(query_tiles(x, causal, first)));
+        }
+        __syncwarp();
       }
     }
   };
-  // Offsets that are not in order can describe more tiles than the lists hold:
-  // then nothing is listed (the error word says so).
   int64_t total = 0;
   each(true, [&](const Tile&, int bq, int bk) {
     atomicAdd(&hist[0][bq], 1);
@@ -117,15 +158,17 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const int64_t* 
     total = n;
   }
   __syncthreads();
+  // Offsets that are not in order can describe more tiles than the lists hold:
+  // then nothing is listed (the error word says so).
   const int64_t most = T / kTile + (S < T ? S : T);
   if (total > most) {
     if (threadIdx.x == 0) {
       set_err(err, FS_ERR_BAD_OFFSETS);
-      *ntiles = 0;
+      plan->ntiles = 0;
     }
     return;
   }
-  if (threadIdx.x == 0) *ntiles = int32_t(total);
+  if (threadIdx.x == 0) plan->ntiles = int32_t(total);
   each(false, [&](const Tile& x, int bq, int bk) {
     by_query[atomicAdd(&hist[0][bq], 1)] = x;
     if (by_key) by_key[atomicAdd(&hist[1][bk], 1)] = x;
@@ -135,41 +178,47 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const int64_t* 
 // ------------------------------------------------------------- shared pieces
 
 struct AttnArgs {
-  const int32_t* ntiles;
+  Plan* plan;
   const Tile* tiles;
   int32_t heads, kv_heads;
   int64_t T;
   bool causal;
   float scale;
-  __nv_bfloat16* o;        // forward: out
+  __nv_bfloat16* o;           // forward: out
   const __nv_bfloat16* out;   // backward: out and dout
   const __nv_bfloat16* dout;
   float* lse;
-  float* delta;            // [heads, T]: written by the dq kernel, read by the dk / dv kernel
+  float* delta;               // [heads, T]: written by the dq kernel, read by the dk / dv kernel
   __nv_bfloat16 *dq, *dk, *dv;
   int64_t dq_stride, dk_stride, dv_stride;
   int32_t* err;
   uint64_t wait_ns;
 };
 
-// Wait of a whole warp for a barrier's phase, with a limit; sets the error word when it gives up.
-// The hand-overs between the warps of a block come every few hundred cycles, so it polls without
-// asking to sleep and looks at the clock only now and then.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t phase, const AttnArgs& a) {
+// Wait of one thread for a barrier's phase, with a limit.  The hand-overs
+// between the warps of a block come every few hundred cycles, so it polls
+// without asking to sleep and looks at the clock only now and then.
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t phase, const AttnArgs& a) {
+  if (bulk::try_wait(bar, phase & 1u)) return true;
   uint64_t t0 = 0;
   for (uint32_t polls = 1;; ++polls) {
-    if (__all_sync(0xffffffffu, bulk::try_wait(bar, phase & 1u))) return true;
+    if (bulk::try_wait(bar, phase & 1u)) return true;
     if ((polls & 1023u) == 0) {
       const uint64_t now = bulk::global_ns();
       if (t0 == 0) t0 = now;
-      if (__any_sync(0xffffffffu, now - t0 > a.wait_ns)) break;
+      if (now - t0 > a.wait_ns) break;
     }
   }
-  if ((threadIdx.x & 31) == 0) set_err(a.err, FS_ERR_TIMEOUT);
+  set_err(a.err, FS_ERR_TIMEOUT);
   return false;
 }
 
-// Tile of `rows` DH columns from position y of head h, as DH / 64 boxes (one thread).
+// The same for a whole warp.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t phase, const AttnArgs& a) {
+  return __all_sync(0xffffffffu, poll(bar, phase, a));
+}
+
+// Tile of 128 rows of DH columns from position y of head h, as DH / 64 boxes (one thread).
 template <int DH>
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int h, int y, uint32_t bar) {
 #pragma unroll
@@ -190,12 +239,99 @@ __device__ __forceinline__ void zero_rows(unsigned char* tile, int from) {
   __syncwarp();
 }
 
+// The loading warp's side of a ring of NS tile slots in shared memory, filled in
+// order.  full[s]: the tile has arrived; free[s]: its last reader is done.  A
+// tile with rows past its sample's end arrives on a barrier of its own
+// (tail[2]), is mended here, and only then reported full; the mending waits until the ring
+// would block anyway, at most two tiles outstanding.
+template <int DH, int NS>
+struct Feeder {
+  static constexpr int TB = DH / 64 * kBox;
+  unsigned char* tiles;
+  uint32_t full, free, tail;
+  const AttnArgs& a;
+  uint32_t slot = 0;             // tiles asked for
+  uint32_t tails = 0, mended = 0;
+  int tail_slot[2] = {0, 0}, tail_rows[2] = {0, 0};
+
+  __device__ __forceinline__ Feeder(unsigned char* tiles, uint32_t full, uint32_t free, uint32_t tail, const AttnArgs& a)
+      : tiles(tiles), full(full), free(free), tail(tail), a(a) {}
+
+  __device__ __forceinline__ bool mend() {  // the oldest tail
+    const uint32_t w = mended & 1u;
+    if (!wait(tail + 8 * w, mended >> 1, a)) return false;
+    const int s = w ? tail_slot[1] : tail_slot[0];
+    zero_rows<DH>(tiles + s * TB, w ? tail_rows[1] : tail_rows[0]);
+    if ((threadIdx.x & 31) == 0) tc::arrive(full + 8 * s);
+    ++mended;
+    return true;
+  }
+  __device__ __forceinline__ bool mend_all() {
+    while (mended != tails)
+      if (!mend()) return false;
+    return true;
+  }
+  // The next tile: position y of head h of `map`, the first `valid` rows (of at most 128) the sample's.
+  // mend_tail: whether the other rows must be zero.
+  __device__ __forceinline__ bool put(const CUtensorMap* map, int h, int y, int valid, bool mend_tail) {
+    const int lane = threadIdx.x & 31;
+    const int s = int(slot % NS);
+    if (slot >= NS) {
+      const uint32_t phase = slot / NS - 1;
+      if (mended != tails && !__all_sync(0xffffffffu, bulk::try_wait(free + 8 * s, phase & 1u)) && !mend_all())
+        return false;
+      if (!wait(free + 8 * s, phase, a)) return false;
+    }
+    uint32_t bar = full + 8 * s;
+    if (mend_tail && valid < kTile) {
+      if (tails - mended == 2 && !mend()) return false;
+      const uint32_t w = tails & 1u;
+      bar = tail + 8 * w;
+      if (w) tail_slot[1] = s, tail_rows[1] = valid;
+      else tail_slot[0] = s, tail_rows[0] = valid;
+      ++tails;
+    }
+    if (lane == 0) {
+      bulk::arrive_expect_tx(bar, TB);
+      load_tile<DH>(bulk::smem_addr(tiles) + s * TB, map, h, y, bar);
+    }
+    ++slot;
+    return true;
+  }
+  // After a wait that gave up: every copy still in flight lands first.
+  __device__ __forceinline__ void drain() {
+    for (uint32_t m = mended; m != tails; ++m) bulk::warp_wait(tail + 8 * (m & 1u), (m >> 1) & 1u, a.wait_ns);
+    for (uint32_t s = slot > NS ? slot - NS : 0; s < slot; ++s) {
+      bool tail_tile = false;
+      for (uint32_t m = mended; m != tails; ++m) tail_tile |= uint32_t((m & 1u) ? tail_slot[1] : tail_slot[0]) == s % NS;
+      if (!tail_tile) bulk::warp_wait(full + 8 * (s % NS), (s / NS) & 1u, a.wait_ns);
+    }
+  }
+};
+
+// Units of a block: its own index first, then whatever comes next in the list.
+// The loading warp takes them and leaves them for the others under the
+// barrier that announces the unit's first tiles (ids[4]: no reader is two units behind).
+struct Taker {
+  int64_t units;
+  int32_t* counter;
+  int round = 0;
+  __device__ __forceinline__ int32_t next() {
+    int64_t u = blockIdx.x;
+    if (round++ > 0) {
+      int32_t v = 0;
+      if ((threadIdx.x & 31) == 0) v = atomicAdd(counter, 1);
+      u = int64_t(gridDim.x) + __shfl_sync(0xffffffffu, v, 0);
+    }
+    return u < units ? int32_t(u) : -1;
+  }
+};
+
 // D[128 x 128] = A B^T over DH columns, both tiles K-major.  Called by a whole warp; lane 0 issues.
 template <int DH>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b) {
   constexpr uint32_t id = tc::idesc(kTile, kTile, false);
-  d = tc::uni(d);
-  const uint32_t da = tc::uni(tc::desc_k(a)), db = tc::uni(tc::desc_k(b));
+  const uint32_t da = tc::desc_k(a), db = tc::desc_k(tc::uni(b));
   if ((threadIdx.x & 31) == 0) {
     tc::mma_ss<true>(d, tc::at(da, 0), tc::at(db, 0), id, false);
 #pragma unroll
@@ -211,11 +347,9 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b) {
 template <int DH>
 __device__ __forceinline__ void mma_cols(uint32_t d, uint32_t a0, uint32_t a1, uint32_t b, bool acc) {
   constexpr uint32_t id = tc::idesc(kTile, DH, true);
-  d = tc::uni(d), a0 = tc::uni(a0), a1 = tc::uni(a1);
-  const uint32_t db = tc::uni(tc::desc_mn(b, kBox));
-  const bool on = tc::uni(uint32_t(acc)) != 0;
+  const uint32_t db = tc::desc_mn(tc::uni(b), kBox);
   if ((threadIdx.x & 31) == 0) {
-    tc::mma_ts<true>(d, a0, tc::at(db, 0), id, on);
+    tc::mma_ts<true>(d, a0, tc::at(db, 0), id, acc);
 #pragma unroll
     for (int k = 1; k < kTile / 16; ++k)
       tc::mma_ts<false>(d, (k < 4 ? a0 + 8 * k : a1 + 8 * (k - 4)), tc::at(db, k * 2048), id, true);
@@ -224,7 +358,6 @@ __device__ __forceinline__ void mma_cols(uint32_t d, uint32_t a0, uint32_t a1, u
 
 // Commit by the lane that issues the products.
 __device__ __forceinline__ void commit(uint32_t bar) {
-  bar = tc::uni(bar);
   if ((threadIdx.x & 31) == 0) tc::commit(bar);
 }
 
@@ -244,75 +377,68 @@ __device__ __forceinline__ void store32(__nv_bfloat16* p, const float* x, float 
 template <int DH>
 constexpr int tile_bytes() { return DH / 64 * kBox; }
 
-__device__ __forceinline__ unsigned char* align_smem(unsigned char* p) {
-  return p + ((1024u - (bulk::smem_addr(p) & 1023u)) & 1023u);
-}
+// Place in a ring of NS slots: item i is in slot i % NS, its phase i / NS.
+template <int NS>
+struct Place {
+  int s;
+  uint32_t phase = 0;
+  __device__ __forceinline__ explicit Place(int first) : s(first) {}
+  __device__ __forceinline__ void skip2() {  // two items further on
+    s += 2;
+    if (s >= NS) s -= NS, ++phase;
+  }
+};
+
+__device__ __forceinline__ void wait_for_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;"); }
 
 // ------------------------------------------------------------- forward
 
-// One block per SM works through units: two query tiles that read the same
-// keys and values, so each loaded tile serves two products.  They are the same
-// positions of two query heads that share a key/value head, or, where the
-// number of sharing heads is odd, neighbouring tiles of one head.  A warpgroup
-// per query tile, one row a thread, does the softmax; one warp issues the
-// products, one the loads, which run ahead into the next unit.  Products of one
-// query tile run under the softmax of the other.  Tensor memory: x of each tile in 128
-// columns, p (bf16) over it, o beside them.
-// A softmax thread holds a row of 128 scores: the third warpgroup (loads,
-// products, two idle warps) gives registers to the other two.  384 threads are
-// launched with kFwdRegs each; 2 * 128 * 208 + 128 * 88 is that total.
+// A unit is two query tiles that read the same keys and values, so each loaded
+// tile serves two products: the same positions of two query heads that share a
+// key/value head, or, where the number of sharing heads is odd, neighbouring
+// tiles of one head.  A warpgroup per query tile, one row a thread, does the
+// softmax; one thread issues the products of the two tiles in turn, so that one tile's products run
+// under the other's softmax.  Tensor memory: x of each tile in 128 columns, p (bf16) over it, o
+// beside them.
+//
+// A softmax thread holds a row of 128 scores: the third warpgroup (products and
+// loads) gives registers to the other two.  384 threads are launched with
+// kFwdRegs each; 2 * 128 * 208 + 128 * 88 is that total.
 constexpr int kFwdThreads = 384, kFwdRegs = 168;
-template <int DH> constexpr int fwd_slots() { return DH == 64 ? 8 : 4; }
-template <int DH> constexpr int fwd_smem() { return tile_bytes<DH>() * (2 + fwd_slots<DH>()) + 1024; }
+template <int DH> constexpr int fwd_slots() { return DH == 64 ? 10 : 5; }
+template <int DH> constexpr int fwd_smem() { return tile_bytes<DH>() * (2 + fwd_slots<DH>()); }
 
 struct FwdUnit {
   Tile x;
-  int head[2], row[2];  // query head and tile index of each query tile
-  int nk[2], own[2];    // key tiles of the history, and whether its own tile follows
+  int head0, head1, row0, row1;  // query head and tile index of each query tile
+  int nk0, nk1, own0, own1;      // key tiles of the history, and whether its own tile follows
   int kv_head, common, n;
   bool by_head, both;
 
   __device__ __forceinline__ FwdUnit(const Tile& tile, int part, const AttnArgs& a) : x(tile) {
     const int group = a.heads / a.kv_heads;
     by_head = group % 2 == 0;
-    if (by_head) {
-      head[0] = 2 * part, head[1] = 2 * part + 1;
-      row[0] = row[1] = x.t;
-    } else {
-      head[0] = head[1] = part;
-      row[0] = 2 * x.t, row[1] = 2 * x.t + 1;
-    }
-    kv_head = head[0] / group;
-    both = row[1] * kTile < x.L;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      Tile y = x;
-      y.t = row[i];
-      nk[i] = key_tiles(y, a.causal, own[i]);
-    }
-    if (!both) nk[1] = own[1] = 0;
-    common = max(nk[0], nk[1]);
-    n = common + own[0] + (by_head ? 0 : own[1]);
+    head0 = by_head ? 2 * part : part, head1 = by_head ? 2 * part + 1 : part;
+    row0 = by_head ? x.t : 2 * x.t, row1 = by_head ? x.t : 2 * x.t + 1;
+    kv_head = head0 / group;
+    both = row1 * kTile < x.L;
+    Tile y = x;
+    y.t = row0;
+    nk0 = key_tiles(y, a.causal, own0);
+    y.t = row1;
+    nk1 = key_tiles(y, a.causal, own1);
+    if (!both) nk1 = own1 = 0;
+    common = max(nk0, nk1);
+    n = common + own0 + (by_head ? 0 : own1);
   }
   // The unit's j-th key tile, and whether query tile i meets it.
   __device__ __forceinline__ int key_tile(int j) const {
-    return j < common ? j : ((j == common && own[0]) || by_head ? row[0] : row[1]);
+    return j < common ? j : ((j == common && own0) || by_head ? row0 : row1);
   }
   __device__ __forceinline__ bool meets(int i, int j) const {
     if (by_head) return true;
-    return i ? j < nk[1] || (own[1] && j == common + own[0]) : j < nk[0] || (own[0] && j == common);
-  }
-};
-
-// Units of this block: dealt out in rounds, back and forth, most work first.
-struct Deal {
-  int64_t units;
-  int64_t round = 0;
-  __device__ __forceinline__ int64_t next() {
-    const int64_t g = gridDim.x, b = blockIdx.x;
-    const int64_t u = round * g + ((round & 1) ? g - 1 - b : b);
-    ++round;
-    return u < units ? u : -1;
+    return i ? j < nk1 || (own1 && j == common + own0) : j < nk0 || (own0 && j == common);
   }
 };
 
@@ -322,109 +448,114 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
                                                                   const __grid_constant__ CUtensorMap mv, AttnArgs a,
                                                                   int parts) {
   constexpr int TB = tile_bytes<DH>(), NS = fwd_slots<DH>();
-  extern __shared__ unsigned char raw[];
-  __shared__ __align__(8) uint64_t bars[8 + 2 * NS];
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ __align__(8) uint64_t bars[12 + 2 * NS];
   __shared__ uint32_t tmem_at;
-  const int64_t units = int64_t(*a.ntiles) * parts;
-  if (int64_t(blockIdx.x) >= units) return;
-  unsigned char* smem = align_smem(raw);
+  __shared__ volatile int32_t ids[4];
   const uint32_t q_at = bulk::smem_addr(smem), kv_at = q_at + 2 * TB;
   const uint32_t bar = bulk::smem_addr(bars);
-  const uint32_t q_full = bar, q_free = bar + 8, s_full = bar + 16, p_ready = bar + 32, o_full = bar + 48, drain = bar + 56,
-                 full = bar + 64, free = bar + 64 + 8 * NS;
+  const uint32_t q_full = bar, q_free = bar + 8, s_full = bar + 16, p_ready = bar + 32, o_full = bar + 48, tail = bar + 64,
+                 drain = bar + 80, full = bar + 96, free = full + 8 * NS;
   const int warp = int(tc::uni(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (warp == 8) {
     if (lane == 0) {
-      for (int i = 0; i < 8 + 2 * NS; ++i) bulk::mbar_init(bar + 8 * i, i == 4 || i == 5 ? 4 : 1);
+      for (int i = 0; i < 12 + 2 * NS; ++i)
+        bulk::mbar_init(bar + 8 * i, i == 1 ? 9 : (i == 4 || i == 5 ? 4 : 1));
       bulk::fence_init();
     }
     __syncwarp();
     tc::alloc(&tmem_at, 512);
     tc::fence_before();
+  } else if (warp == 9 && lane == 0) {
+    tc::prefetch_map(&mq), tc::prefetch_map(&mk), tc::prefetch_map(&mv);
   }
   __syncthreads();
   tc::fence_after();
-  const uint32_t s_at = tmem_at, o_at = tmem_at + 256;  // of query tile 0; tile 1's follow
-  Deal deal{units};
-  bool ok = true;
+  wait_for_launch();
+  const uint32_t s_at = tc::uni(tmem_at), o_at = s_at + 256;  // of query tile 0; tile 1's follow
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 9) {
-    // loads: the two query tiles of a unit, then its key and value tiles, in order, through NS slots
-    int64_t slot = 0;
-    for (int k = 0;; ++k) {
-      const int64_t u = deal.next();
-      if (u < 0) break;
-      const FwdUnit f(a.tiles[u / parts], int(u % parts), a);
-      if (k > 0 && !(ok = wait(q_free, k - 1, a))) break;
-      if (lane == 0) {
-        bulk::arrive_expect_tx(q_full, f.both ? 2 * TB : TB);
-        load_tile<DH>(q_at, &mq, f.head[0], f.x.begin + f.row[0] * kTile, q_full);
-        if (f.both) load_tile<DH>(q_at + TB, &mq, f.head[1], f.x.begin + f.row[1] * kTile, q_full);
-      }
-      for (int j = 0; ok && j < 2 * f.n; ++j, ++slot) {
-        const int s = int(slot % NS);
-        if (slot >= NS && !(ok = wait(free + 8 * s, uint32_t(slot / NS - 1), a))) break;
+      Feeder<DH, NS> feed(smem + 2 * TB, full, free, tail, a);
+      Taker take{int64_t(a.plan->ntiles) * parts, &a.plan->next[0]};
+      bool ok = true;
+      int k = 0;
+      for (;; ++k) {
+        const int32_t u = take.next();
+        if (k > 0 && !(ok = feed.mend_all() && wait(q_free, k - 1, a))) break;
+        if (lane == 0) ids[k & 3] = u;
+        if (u < 0) {
+          if (lane == 0) tc::arrive(q_full);
+          break;
+        }
+        const FwdUnit f(a.tiles[u / parts], u % parts, a);
         if (lane == 0) {
-          bulk::arrive_expect_tx(full + 8 * s, TB);
-          load_tile<DH>(kv_at + s * TB, j & 1 ? &mv : &mk, f.kv_head, f.x.begin + f.key_tile(j >> 1) * kTile,
-                        full + 8 * s);
+          bulk::arrive_expect_tx(q_full, f.both ? 2 * TB : TB);
+          load_tile<DH>(q_at, &mq, f.head0, f.x.begin + f.row0 * kTile, q_full);
+          if (f.both) load_tile<DH>(q_at + TB, &mq, f.head1, f.x.begin + f.row1 * kTile, q_full);
         }
-      }
-      if (!ok) break;
-    }
-    if (!ok)  // gave up: let what is in flight land
-      for (int64_t s = slot > NS ? slot - NS : 0; s < slot; ++s)
-        bulk::warp_wait(full + 8 * int(s % NS), uint32_t(s / NS) & 1u, a.wait_ns);
-    } else if (warp == 8) {
-    // products: at step j, o += p v of key tile j - 1 and x of key tile j, of query tile 0, then of 1
-    int64_t slot = 0;           // of the unit's first key tile
-    uint32_t done[2] = {0, 0};  // p's consumed
-    for (int k = 0; ok; ++k) {
-      const int64_t u = deal.next();
-      if (u < 0) break;
-      const FwdUnit f(a.tiles[u / parts], int(u % parts), a);
-      if (!(ok = wait(q_full, k, a))) break;
-      uint32_t acc[2] = {0, 0};
-      for (int j = 0; j <= f.n; ++j) {
-        const int64_t ks = slot + 2 * j, vs = ks - 1;  // slots of key tile j and value tile j - 1
-        const uint32_t k_tile = kv_at + uint32_t(ks % NS) * TB, v_tile = kv_at + uint32_t(vs % NS + NS) % NS * TB;
-        if (j > 0) {
-          if (!(ok = wait(full + 8 * int(vs % NS), uint32_t(vs / NS), a))) break;
-          const int valid = f.x.L - f.key_tile(j - 1) * kTile;
-          if (valid < kTile) zero_rows<DH>(smem + 2 * TB + int(vs % NS) * TB, valid);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (i == 1 && !f.both) continue;
-          if (j > 0 && f.meets(i, j - 1)) {
-            if (!(ok = wait(p_ready + 8 * i, done[i], a))) break;
-            ++done[i];
-            tc::fence_after();
-            mma_cols<DH>(o_at + i * DH, s_at + 128 * i, s_at + 128 * i + 32, v_tile, acc[i] != 0);
-            acc[i] = 1;
-          }
-          if (j < f.n && f.meets(i, j)) {
-            // x overwrites p: the products execute in the order they are issued
-            if (!(ok = wait(full + 8 * int(ks % NS), uint32_t(ks / NS), a))) break;
-            mma_rows<DH>(s_at + 128 * i, q_at + i * TB, k_tile);
-            commit(s_full + 8 * i);
-          }
+        for (int j = 0; ok && j < f.n; ++j) {
+          const int at = f.key_tile(j) * kTile;
+          ok = feed.put(&mk, f.kv_head, f.x.begin + at, f.x.L - at, false) &&
+               feed.put(&mv, f.kv_head, f.x.begin + at, f.x.L - at, true);
         }
         if (!ok) break;
-        if (j > 0) commit(free + 8 * int(vs % NS));
-        if (j < f.n) commit(free + 8 * int(ks % NS));
-        if (j == f.n - 1) commit(q_free);
-        if (j == f.n) commit(o_full);
       }
-      slot += 2 * f.n;
+      if (!ok) {
+        bulk::warp_wait(q_full, uint32_t(k) & 1u, a.wait_ns);
+        feed.drain();
+      }
+    } else if (warp == 8) {
+      // products: at step j, o += p v of key tile j - 1 and x of key tile j, of query tile 0, then of 1
+      // (one issuing thread: two would fall into step, and both tiles' softmax would wait together)
+      Place<NS> ks(0), vs(1);
+      uint32_t done[2] = {0, 0};  // p's consumed
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        if (!(ok = wait(q_full, k, a))) break;
+        const int32_t u = ids[k & 3];
+        if (u < 0) break;
+        const FwdUnit f(a.tiles[u / parts], u % parts, a);
+        bool acc[2] = {false, false};
+        for (int j = 0; j <= f.n; ++j) {
+          if (j > 0 && !(ok = wait(full + 8 * vs.s, vs.phase, a))) break;
+          if (j < f.n && !(ok = wait(full + 8 * ks.s, ks.phase, a))) break;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (i == 1 && !f.both) continue;
+            if (j > 0 && f.meets(i, j - 1)) {
+              if (!(ok = wait(p_ready + 8 * i, done[i], a))) break;
+              ++done[i];
+              tc::fence_after();
+              mma_cols<DH>(o_at + DH * i, s_at + 128 * i, s_at + 128 * i + 32, kv_at + vs.s * TB, acc[i]);
+              acc[i] = true;
+            }
+            if (j < f.n && f.meets(i, j)) {
+              // x overwrites p: the products execute in the order they are issued
+              mma_rows<DH>(s_at + 128 * i, q_at + i * TB, kv_at + ks.s * TB);
+              commit(s_full + 8 * i);
+            }
+          }
+          if (!ok) break;
+          if (j > 0) {
+            commit(free + 8 * vs.s);
+            vs.skip2();
+          }
+          if (j < f.n) {
+            commit(free + 8 * ks.s);
+            ks.skip2();
+          }
+          if (j == f.n - 1) commit(q_free);
+          if (j == f.n) commit(o_full);
+        }
+      }
+      if (!ok) {
+        commit(drain);
+        wait(drain, 0, a);
+      }
     }
-    if (!ok) {
-      if (lane == 0) tc::commit(drain);
-      bulk::warp_wait(drain, 0, a.wait_ns);
-    }
-    }
+    __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int i = warp >> 2;  // query tile of this warpgroup
@@ -432,16 +563,24 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
     const uint32_t x_at = s_at + 128 * i + lanes, acc_at = o_at + DH * i + lanes;
     const float c = a.scale * kLog2e;
     uint32_t seen = 0;
+    bool ok = true;
     for (int k = 0; ok; ++k) {
-      const int64_t u = deal.next();
+      if (!(ok = wait(q_full, k, a))) break;
+      const int32_t u = ids[k & 3];
       if (u < 0) break;
-      const FwdUnit f(a.tiles[u / parts], int(u % parts), a);
-      const int tile = i ? f.row[1] : f.row[0];
+      __syncwarp();
+      if (lane == 0) tc::arrive(q_free);  // (a warpgroup without work in this unit keeps step with the others)
+      const FwdUnit f(a.tiles[u / parts], u % parts, a);
+      if (i == 1 && !f.both) {
+        if (!(ok = wait(o_full, k, a))) break;
+        continue;
+      }
+      const int tile = i ? f.row1 : f.row0;
       const int row = tile * kTile + int(threadIdx.x & 127);  // position inside the sample
       float m = -INFINITY, l = 0.f;
       bool first = true;
       for (int j = 0; j < f.n; ++j) {
-        if ((i == 1 && !f.both) || !f.meets(i, j)) continue;
+        if (!f.meets(i, j)) continue;
         if (!(ok = wait(s_full + 8 * i, seen, a))) break;
         ++seen;
         tc::fence_after();
@@ -513,9 +652,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
       }
       if (!ok || !(ok = wait(o_full, k, a))) break;
       tc::fence_after();
-      if (i == 1 && !f.both) continue;
       const int64_t pos = int64_t(f.x.begin) + row;
-      const int head = i ? f.head[1] : f.head[0];
+      const int head = i ? f.head1 : f.head0;
       const float inv = 1.f / l;
 #pragma unroll
       for (int b = 0; b < DH / 32; ++b) {
@@ -532,17 +670,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
   __syncthreads();
   if (warp == 8) {
     tc::fence_after();
-    tc::dealloc(tmem_at, 512);
+    tc::dealloc(s_at, 512);
   }
 }
 
 // ------------------------------------------------------------- backward
 
-constexpr int kBwdThreads = 288;  // eight warps for the elementwise part, one for loads and products
-template <int DH> constexpr int bwd_smem() { return tile_bytes<DH>() * 6 + 1024; }
+constexpr int kBwdThreads = 320;  // eight warps for the elementwise part, one for products, one for loads
+template <int DH> constexpr int bwd_slots() { return DH == 64 ? 10 : 5; }
+template <int DH> constexpr int bwd_smem() { return tile_bytes<DH>() * (2 + bwd_slots<DH>()); }
 
-// dq of one query tile and head.  A thread holds one query row and 64 of the
-// 128 keys.  Per key tile: x = q k^T and do v^T into 128 columns each; p = exp(x - lse)
+// dq of one query tile and head a unit.  A thread holds one query row and 64 of
+// the 128 keys.  Per key tile: x = q k^T and do v^T into 128 columns each; p = exp(x - lse)
 // stays in registers and frees x, so the next tile's x is computed while
 // ds = p * (do v^T - delta) is formed; ds (bf16) goes over do v^T and multiplies k.
 template <int DH>
@@ -550,190 +689,203 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                                                                  const __grid_constant__ CUtensorMap mk,
                                                                  const __grid_constant__ CUtensorMap mv,
                                                                  const __grid_constant__ CUtensorMap mdo, AttnArgs a) {
-  constexpr int TB = tile_bytes<DH>();
-  extern __shared__ unsigned char raw[];
-  __shared__ __align__(8) uint64_t bars[12];
+  constexpr int TB = tile_bytes<DH>(), NS = bwd_slots<DH>();
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ __align__(8) uint64_t bars[11 + 2 * NS];
   __shared__ uint32_t tmem_at;
+  __shared__ volatile int32_t ids[4];
   __shared__ float half_delta[2][kTile];
-  const int head = int(blockIdx.x % unsigned(a.heads));
-  const int64_t at = blockIdx.x / unsigned(a.heads);
-  if (at >= *a.ntiles) return;
-  const Tile x = a.tiles[at];
-  const int kv_head = head / (a.heads / a.kv_heads);
-  int own;
-  const int nk = key_tiles(x, a.causal, own);
-  const int n = nk + own;
-  unsigned char* smem = align_smem(raw);
-  const uint32_t q_at = bulk::smem_addr(smem), do_at = q_at + TB, k_at = do_at + TB, v_at = k_at + 2 * TB;
+  const uint32_t q_at = bulk::smem_addr(smem), do_at = q_at + TB, kv_at = do_at + TB;
   const uint32_t bar = bulk::smem_addr(bars);
-  const uint32_t q_full = bar, k_full = bar + 8, v_full = bar + 24, s_full = bar + 40, dp_full = bar + 48,
-                 s_read = bar + 56, ds_ready = bar + 64, dq_done = bar + 72, drain = bar + 80, fin = bar + 88;
+  const uint32_t q_full = bar, q_free = bar + 8, s_full = bar + 16, dp_full = bar + 24, s_read = bar + 32,
+                 ds_ready = bar + 40, delta_in = bar + 48, dq_full = bar + 56, tail = bar + 64, drain = bar + 80,
+                 full = bar + 88, free = full + 8 * NS;
   const int warp = int(tc::uni(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (warp == 8) {
     if (lane == 0) {
-      tc::prefetch_map(&mq), tc::prefetch_map(&mk), tc::prefetch_map(&mv), tc::prefetch_map(&mdo);
-      for (int i = 0; i < 12; ++i) bulk::mbar_init(bar + 8 * i, i == 7 || i == 8 ? 8 : 1);
+      for (int i = 0; i < 11 + 2 * NS; ++i) bulk::mbar_init(bar + 8 * i, i >= 4 && i <= 6 ? 8 : 1);
       bulk::fence_init();
     }
     __syncwarp();
     tc::alloc(&tmem_at, 512);
     tc::fence_before();
+  } else if (warp == 9 && lane == 0) {
+    tc::prefetch_map(&mq), tc::prefetch_map(&mk), tc::prefetch_map(&mv), tc::prefetch_map(&mdo);
   }
   __syncthreads();
   tc::fence_after();
-  const uint32_t s_at = tmem_at, dp_at = tmem_at + 128, dq_at = tmem_at + 256;
-  auto key_tile = [&](int j) { return j < nk ? j : x.t; };
+  wait_for_launch();
+  let_next_launch();
+  const uint32_t s_at = tc::uni(tmem_at), dp_at = s_at + 128, dq_at = s_at + 256;
+  const int group = a.heads / a.kv_heads;
 
-  if (warp == 8) {
-    int loaded_k = 0, loaded_v = 0;
-    auto load_k = [&](int j) {
+  if (warp == 9) {
+    Feeder<DH, NS> feed(smem + 2 * TB, full, free, tail, a);
+    Taker take{int64_t(a.plan->ntiles) * a.heads, &a.plan->next[0]};
+    bool ok = true;
+    int k = 0;
+    for (;; ++k) {
+      const int32_t u = take.next();
+      if (k > 0 && !(ok = feed.mend_all() && wait(q_free, k - 1, a))) break;
+      if (lane == 0) ids[k & 3] = u;
+      if (u < 0) {
+        if (lane == 0) tc::arrive(q_full);
+        break;
+      }
+      const Tile x = a.tiles[u / a.heads];
+      const int head = u % a.heads, kv_head = head / group;
+      int own;
+      const int nk = key_tiles(x, a.causal, own), n = nk + own;
       if (lane == 0) {
-        bulk::arrive_expect_tx(k_full + 8 * (j & 1), TB);
-        load_tile<DH>(k_at + (j & 1) * TB, &mk, kv_head, x.begin + key_tile(j) * kTile, k_full + 8 * (j & 1));
+        bulk::arrive_expect_tx(q_full, 2 * TB);
+        load_tile<DH>(q_at, &mq, head, x.begin + x.t * kTile, q_full);
+        load_tile<DH>(do_at, &mdo, head, x.begin + x.t * kTile, q_full);
       }
-      loaded_k = j + 1;
-    };
-    auto load_v = [&](int j) {
-      if (lane == 0) {
-        bulk::arrive_expect_tx(v_full + 8 * (j & 1), TB);
-        load_tile<DH>(v_at + (j & 1) * TB, &mv, kv_head, x.begin + key_tile(j) * kTile, v_full + 8 * (j & 1));
+      for (int j = 0; ok && j < n; ++j) {
+        const int at = (j < nk ? j : x.t) * kTile;
+        ok = feed.put(&mk, kv_head, x.begin + at, x.L - at, true) && feed.put(&mv, kv_head, x.begin + at, x.L - at, false);
       }
-      loaded_v = j + 1;
-    };
-    auto key_ready = [&](int j) {
-      if (!wait(k_full + 8 * (j & 1), j >> 1, a)) return false;
-      const int valid = x.L - key_tile(j) * kTile;
-      if (valid < kTile) zero_rows<DH>(smem + TB * (2 + (j & 1)), valid);
-      return true;
-    };
-    if (lane == 0) {
-      bulk::arrive_expect_tx(q_full, 2 * TB);
-      load_tile<DH>(q_at, &mq, head, x.begin + x.t * kTile, q_full);
-      load_tile<DH>(do_at, &mdo, head, x.begin + x.t * kTile, q_full);
-    }
-    for (int j = 0; j < 2 && j < n; ++j) {
-      load_k(j);
-      load_v(j);
-    }
-    bool ok = wait(q_full, 0, a) && key_ready(0) && wait(v_full, 0, a);
-    if (ok) {
-      mma_rows<DH>(s_at, q_at, k_at);
-      commit(s_full);
-      mma_rows<DH>(dp_at, do_at, v_at);
-      commit(dp_full);
-    }
-    for (int j = 0; ok && j < n; ++j) {
-      const int st = j & 1, nx = st ^ 1;
-      if (j + 1 < n) {
-        if (!(ok = key_ready(j + 1) && wait(s_read, j, a))) break;
-        tc::fence_after();
-        mma_rows<DH>(s_at, q_at, k_at + nx * TB);
-        commit(s_full);
-      }
-      if (!(ok = wait(ds_ready, j, a))) break;
-      tc::fence_after();
-      mma_cols<DH>(dq_at, dp_at, dp_at + 64, k_at + st * TB, j != 0);
-      commit(j + 1 < n ? dq_done : fin);
-      if (j + 1 < n) {
-        if (!(ok = wait(v_full + 8 * nx, (j + 1) >> 1, a))) break;
-        // do v^T overwrites ds: the products execute in the order they are issued
-        mma_rows<DH>(dp_at, do_at, v_at + nx * TB);
-        commit(dp_full);
-      }
-      if (j + 2 < n) {
-        load_v(j + 2);  // (ds_ready: the product that read this stage is done)
-        if (!(ok = wait(dq_done, j, a))) break;
-        load_k(j + 2);
-      }
+      if (!ok) break;
     }
     if (!ok) {
-      if (lane == 0) tc::commit(drain);
-      bulk::warp_wait(drain, 0, a.wait_ns);
-      bulk::warp_wait(q_full, 0, a.wait_ns);
-      for (int s = 0; s < 2; ++s) {
-        if (loaded_k > s) bulk::warp_wait(k_full + 8 * s, ((loaded_k - 1 - s) >> 1) & 1, a.wait_ns);
-        if (loaded_v > s) bulk::warp_wait(v_full + 8 * s, ((loaded_v - 1 - s) >> 1) & 1, a.wait_ns);
+      bulk::warp_wait(q_full, uint32_t(k) & 1u, a.wait_ns);
+      feed.drain();
+    }
+  } else if (warp == 8) {
+    Place<NS> ks(0), vs(1), kq(0);  // next key and value tile to read, and the key tile of the next dq product
+    uint32_t c = 0;                 // key tiles so far
+    bool ok = true;
+    auto scores = [&]() {           // x of the next key tile, into columns that the last tile's readers have left
+      if (!wait(full + 8 * ks.s, ks.phase, a) || (c > 0 && !wait(s_read, c - 1, a))) return false;
+      tc::fence_after();
+      mma_rows<DH>(s_at, q_at, kv_at + ks.s * TB);
+      commit(s_full);
+      ks.skip2();
+      return true;
+    };
+    auto products = [&]() {  // do v^T of the next value tile, over ds: the products execute in the order they are issued
+      if (!wait(full + 8 * vs.s, vs.phase, a)) return false;
+      mma_rows<DH>(dp_at, do_at, kv_at + vs.s * TB);
+      commit(dp_full);
+      commit(free + 8 * vs.s);
+      vs.skip2();
+      return true;
+    };
+    for (int k = 0; ok; ++k) {
+      if (!(ok = wait(q_full, k, a))) break;
+      const int32_t u = ids[k & 3];
+      if (u < 0) break;
+      const Tile x = a.tiles[u / a.heads];
+      int own;
+      const int nk = key_tiles(x, a.causal, own), n = nk + own;
+      if (!(ok = scores() && products())) break;
+      for (int j = 0; j < n; ++j) {
+        ++c;
+        if (j + 1 < n && !(ok = scores())) break;
+        if (j + 1 == n) commit(q_free);
+        if (!(ok = wait(ds_ready, c - 1, a))) break;
+        tc::fence_after();
+        mma_cols<DH>(dq_at, dp_at, dp_at + 64, kv_at + kq.s * TB, j != 0);
+        commit(free + 8 * kq.s);
+        kq.skip2();
+        if (j + 1 < n && !(ok = products())) break;
       }
+      if (ok) commit(dq_full);
+    }
+    if (!ok) {
+      commit(drain);
+      wait(drain, 0, a);
     }
   } else {
     const int r = threadIdx.x & 127, half = threadIdx.x >> 7;
-    const int row = x.t * kTile + r;
-    const bool live = row < x.L;
-    const int64_t pos = int64_t(x.begin) + row;
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t cols = 64 * half;
     const float c = a.scale * kLog2e;
-    // delta = dout.out of the row, half of the columns each
-    float d = 0.f;
-    if (live) {
-      const uint4* po = reinterpret_cast<const uint4*>(a.out + (pos * a.heads + head) * DH + half * (DH / 2));
-      const uint4* pg = reinterpret_cast<const uint4*>(a.dout + (pos * a.heads + head) * DH + half * (DH / 2));
-#pragma unroll
-      for (int i = 0; i < DH / 16; ++i) {
-        const uint4 u = __ldg(po + i), w = __ldg(pg + i);
-        const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          d = fmaf(__uint_as_float(uu[q] << 16), __uint_as_float(ww[q] << 16), d);
-          d = fmaf(__uint_as_float(uu[q] & 0xFFFF0000u), __uint_as_float(ww[q] & 0xFFFF0000u), d);
-        }
-      }
-    }
-    half_delta[half][r] = d;
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    const float delta = half_delta[0][r] + half_delta[1][r];
-    if (live && half == 0) a.delta[int64_t(head) * a.T + pos] = delta;
-    const float lse2 = live ? a.lse[int64_t(head) * a.T + pos] * kLog2e : 0.f;
+    uint32_t seen = 0;
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      if (!(ok = wait(s_full, j, a))) break;
-      tc::fence_after();
-      float p[64];
-      tc::ld32(s_at + lanes + cols, p);
-      tc::ld32(s_at + lanes + cols + 32, p + 32);
-      tc::wait_ld();
-      tc::tie32(p);
-      tc::tie32(p + 32);
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::arrive(s_read);
-      const int k0 = key_tile(j) * kTile + int(cols);
-      const bool masked = k0 - int(cols) + kTile > x.uih || (a.causal && k0 - int(cols) + kTile > x.t * kTile);
-      const int lim = (a.causal ? min(x.uih, row + 1) : x.uih) - k0, self = row - k0;
+    for (int k = 0; ok; ++k) {
+      if (!(ok = wait(q_full, k, a))) break;
+      const int32_t u = ids[k & 3];
+      if (u < 0) break;
+      const Tile x = a.tiles[u / a.heads];
+      const int head = u % a.heads;
+      int own;
+      const int nk = key_tiles(x, a.causal, own), n = nk + own;
+      const int row = x.t * kTile + r;
+      const bool live = row < x.L;
+      const int64_t pos = int64_t(x.begin) + row;
+      // delta = dout.out of the row, half of the columns each
+      float d = 0.f, lse2 = 0.f;
+      if (live) {
+        lse2 = a.lse[int64_t(head) * a.T + pos] * kLog2e;
+        const uint4* po = reinterpret_cast<const uint4*>(a.out + (pos * a.heads + head) * DH + half * (DH / 2));
+        const uint4* pg = reinterpret_cast<const uint4*>(a.dout + (pos * a.heads + head) * DH + half * (DH / 2));
 #pragma unroll
-      for (int i = 0; i < 64; i += 2) {
-        tc::fma2(p + i, c, c, -lse2, -lse2);
-        p[i] = tc::ex2(p[i]);
-        p[i + 1] = tc::ex2(p[i + 1]);
+        for (int i = 0; i < DH / 16; ++i) {
+          const uint4 v = __ldg(po + i), w = __ldg(pg + i);
+          const uint32_t vv[4] = {v.x, v.y, v.z, v.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            d = fmaf(__uint_as_float(vv[q] << 16), __uint_as_float(ww[q] << 16), d);
+            d = fmaf(__uint_as_float(vv[q] & 0xFFFF0000u), __uint_as_float(ww[q] & 0xFFFF0000u), d);
+          }
+        }
       }
-      if (!(ok = wait(dp_full, j, a))) break;
-      tc::fence_after();
-      uint32_t w[32];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        float g[32];
-        tc::ld32(dp_at + lanes + cols + 32 * b, g);
+      half_delta[half][r] = d;
+      __syncwarp();
+      if (lane == 0) tc::arrive(delta_in);
+      if (!(ok = wait(delta_in, k, a))) break;
+      const float delta = half_delta[0][r] + half_delta[1][r];
+      if (live && half == 0) a.delta[int64_t(head) * a.T + pos] = delta;
+      for (int j = 0; j < n; ++j, ++seen) {
+        if (!(ok = wait(s_full, seen, a))) break;
+        tc::fence_after();
+        float p[64];
+        tc::ld32(s_at + lanes + cols, p);
+        tc::ld32(s_at + lanes + cols + 32, p + 32);
         tc::wait_ld();
-        tc::tie32(g);
+        tc::tie32(p);
+        tc::tie32(p + 32);
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::arrive(s_read);
+        const int t0 = (j < nk ? j : x.t) * kTile, k0 = t0 + int(cols);
+        const bool masked = t0 + kTile > x.uih || (a.causal && t0 + kTile > x.t * kTile);
+        const int lim = (a.causal ? min(x.uih, row + 1) : x.uih) - k0, self = row - k0;
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          tc::add2(g + i, -delta, -delta);
-          tc::mul2(g + i, p[32 * b + i], p[32 * b + i + 1]);
+        for (int i = 0; i < 64; i += 2) {
+          tc::fma2(p + i, c, c, -lse2, -lse2);
+          p[i] = tc::ex2(p[i]);
+          p[i + 1] = tc::ex2(p[i + 1]);
         }
-        if (masked) {
+        if (!(ok = wait(dp_full, seen, a))) break;
+        tc::fence_after();
+        uint32_t w[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) g[i] = (32 * b + i < lim || 32 * b + i == self) ? g[i] : 0.f;
+        for (int b = 0; b < 2; ++b) {
+          float g[32];
+          tc::ld32(dp_at + lanes + cols + 32 * b, g);
+          tc::wait_ld();
+          tc::tie32(g);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            tc::add2(g + i, -delta, -delta);
+            tc::mul2(g + i, p[32 * b + i], p[32 * b + i + 1]);
+          }
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) g[i] = (32 * b + i < lim || 32 * b + i == self) ? g[i] : 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) w[16 * b + i / 2] = tc::pack2(g[i], g[i + 1]);
         }
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) w[16 * b + i / 2] = tc::pack2(g[i], g[i + 1]);
+        tc::st32(dp_at + lanes + cols, w);
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::arrive(ds_ready);
       }
-      tc::st32(dp_at + lanes + cols, w);
-      tc::wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::arrive(ds_ready);
-    }
-    if (ok && wait(fin, 0, a)) {
+      if (!ok || !(ok = wait(dq_full, k, a))) break;
       tc::fence_after();
 #pragma unroll
       for (int b = 0; b < DH / 64; ++b) {
@@ -750,11 +902,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
   __syncthreads();
   if (warp == 8) {
     tc::fence_after();
-    tc::dealloc(tmem_at, 512);
+    tc::dealloc(s_at, 512);
   }
 }
 
-// dk and dv of one key tile and key/value head, over the query heads that
+// dk and dv of one key tile and key/value head a unit, over the query heads that
 // share it and the query tiles that see it.  A thread holds one key and 64 of
 // the 128 queries (everything transposed: x^T = k q^T, v do^T).  p^T (bf16)
 // goes over x^T and multiplies do, then the next x^T is computed while
@@ -764,189 +916,210 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                                                                   const __grid_constant__ CUtensorMap mk,
                                                                   const __grid_constant__ CUtensorMap mv,
                                                                   const __grid_constant__ CUtensorMap mdo, AttnArgs a) {
-  constexpr int TB = tile_bytes<DH>();
-  extern __shared__ unsigned char raw[];
-  __shared__ __align__(8) uint64_t bars[10];
+  constexpr int TB = tile_bytes<DH>(), NS = bwd_slots<DH>();
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ __align__(8) uint64_t bars[11 + 2 * NS];
   __shared__ uint32_t tmem_at;
+  __shared__ volatile int32_t ids[4];
   __shared__ __align__(16) float row_lse[2][kTile], row_delta[2][kTile];
-  const int kv_head = int(blockIdx.x % unsigned(a.kv_heads));
-  const int64_t at = blockIdx.x / unsigned(a.kv_heads);
-  if (at >= *a.ntiles) return;
-  const Tile x = a.tiles[at];
-  const int group = a.heads / a.kv_heads;
-  int first;
-  const int nq = query_tiles(x, a.causal, first);
-  const int n = nq * group;
-  unsigned char* smem = align_smem(raw);
-  const uint32_t k_at = bulk::smem_addr(smem), v_at = k_at + TB, q_at = v_at + TB;  // then two stages of (q, do)
+  const uint32_t k_at = bulk::smem_addr(smem), v_at = k_at + TB, qd_at = v_at + TB;
   const uint32_t bar = bulk::smem_addr(bars);
-  const uint32_t k_full = bar, q_full = bar + 8, s_full = bar + 24, dp_full = bar + 32, p_ready = bar + 40,
-                 ds_ready = bar + 48, done = bar + 56, drain = bar + 64, fin = bar + 72;
+  const uint32_t kv_full = bar, kv_free = bar + 8, s_full = bar + 16, dp_full = bar + 24, p_ready = bar + 32,
+                 ds_ready = bar + 40, rows_in = bar + 48, sums_full = bar + 56, tail = bar + 64, drain = bar + 80,
+                 full = bar + 88, free = full + 8 * NS;
   const int warp = int(tc::uni(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (warp == 8) {
     if (lane == 0) {
-      tc::prefetch_map(&mq), tc::prefetch_map(&mk), tc::prefetch_map(&mv), tc::prefetch_map(&mdo);
-      for (int i = 0; i < 10; ++i) bulk::mbar_init(bar + 8 * i, i == 5 || i == 6 ? 8 : 1);
+      for (int i = 0; i < 11 + 2 * NS; ++i) bulk::mbar_init(bar + 8 * i, i >= 4 && i <= 6 ? 8 : 1);
       bulk::fence_init();
     }
     __syncwarp();
     tc::alloc(&tmem_at, 512);
     tc::fence_before();
+  } else if (warp == 9 && lane == 0) {
+    tc::prefetch_map(&mq), tc::prefetch_map(&mk), tc::prefetch_map(&mv), tc::prefetch_map(&mdo);
   }
   __syncthreads();
   tc::fence_after();
-  const uint32_t s_at = tmem_at, dp_at = tmem_at + 128, dv_at = tmem_at + 256, dk_at = tmem_at + 256 + DH;
-  auto query_tile = [&](int j) { return first + j % nq; };
-  auto query_head = [&](int j) { return kv_head * group + j / nq; };
+  wait_for_launch();
+  const uint32_t s_at = tc::uni(tmem_at), dp_at = s_at + 128, dv_at = s_at + 256, dk_at = s_at + 256 + DH;
+  const int group = a.heads / a.kv_heads;
 
-  if (warp == 8) {
-    int loaded = 0;
-    auto load_q = [&](int j) {
+  if (warp == 9) {
+    Feeder<DH, NS> feed(smem + 2 * TB, full, free, tail, a);
+    Taker take{int64_t(a.plan->ntiles) * a.kv_heads, &a.plan->next[1]};
+    bool ok = true;
+    int k = 0;
+    for (;; ++k) {
+      const int32_t u = take.next();
+      if (k > 0 && !(ok = feed.mend_all() && wait(kv_free, k - 1, a))) break;
+      if (lane == 0) ids[k & 3] = u;
+      if (u < 0) {
+        if (lane == 0) tc::arrive(kv_full);
+        break;
+      }
+      const Tile x = a.tiles[u / a.kv_heads];
+      const int kv_head = u % a.kv_heads;
+      int first;
+      const int nq = query_tiles(x, a.causal, first);
       if (lane == 0) {
-        const uint32_t b = q_full + 8 * (j & 1), to = q_at + (j & 1) * 2 * TB;
-        const int y = x.begin + query_tile(j) * kTile;
-        bulk::arrive_expect_tx(b, 2 * TB);
-        load_tile<DH>(to, &mq, query_head(j), y, b);
-        load_tile<DH>(to + TB, &mdo, query_head(j), y, b);
+        bulk::arrive_expect_tx(kv_full, 2 * TB);
+        load_tile<DH>(k_at, &mk, kv_head, x.begin + x.t * kTile, kv_full);
+        load_tile<DH>(v_at, &mv, kv_head, x.begin + x.t * kTile, kv_full);
       }
-      loaded = j + 1;
-    };
-    auto query_ready = [&](int j) {
-      if (!wait(q_full + 8 * (j & 1), j >> 1, a)) return false;
-      const int valid = x.L - query_tile(j) * kTile;
-      if (valid < kTile) {
-        zero_rows<DH>(smem + TB * (2 + 2 * (j & 1)), valid);
-        zero_rows<DH>(smem + TB * (3 + 2 * (j & 1)), valid);
-      }
-      return true;
-    };
-    if (lane == 0) {
-      bulk::arrive_expect_tx(k_full, 2 * TB);
-      load_tile<DH>(k_at, &mk, kv_head, x.begin + x.t * kTile, k_full);
-      load_tile<DH>(v_at, &mv, kv_head, x.begin + x.t * kTile, k_full);
-    }
-    for (int j = 0; j < 2 && j < n; ++j) load_q(j);
-    bool ok = wait(k_full, 0, a) && query_ready(0);
-    if (ok) {
-      mma_rows<DH>(s_at, k_at, q_at);
-      commit(s_full);
-      mma_rows<DH>(dp_at, v_at, q_at + TB);
-      commit(dp_full);
-    }
-    for (int j = 0; ok && j < n; ++j) {
-      const uint32_t cur = q_at + (j & 1) * 2 * TB, nxt = q_at + ((j + 1) & 1) * 2 * TB;
-      if (j + 1 < n && !(ok = query_ready(j + 1))) break;
-      if (!(ok = wait(p_ready, j, a))) break;
-      tc::fence_after();
-      mma_cols<DH>(dv_at, s_at, s_at + 64, cur + TB, j != 0);
-      if (j + 1 < n) {  // x^T overwrites p^T: the products execute in the order they are issued
-        mma_rows<DH>(s_at, k_at, nxt);
-        commit(s_full);
-      }
-      if (!(ok = wait(ds_ready, j, a))) break;
-      tc::fence_after();
-      mma_cols<DH>(dk_at, dp_at, dp_at + 64, cur, j != 0);
-      commit(j + 1 < n ? done : fin);
-      if (j + 1 < n) {
-        mma_rows<DH>(dp_at, v_at, nxt + TB);
-        commit(dp_full);
-      }
-      if (j + 2 < n) {
-        if (!(ok = wait(done, j, a))) break;
-        load_q(j + 2);
-      }
+      for (int h = kv_head * group; ok && h < (kv_head + 1) * group; ++h)
+        for (int j = 0; ok && j < nq; ++j) {
+          const int at = (first + j) * kTile;
+          ok = feed.put(&mq, h, x.begin + at, x.L - at, true) && feed.put(&mdo, h, x.begin + at, x.L - at, true);
+        }
+      if (!ok) break;
     }
     if (!ok) {
-      if (lane == 0) tc::commit(drain);
-      bulk::warp_wait(drain, 0, a.wait_ns);
-      bulk::warp_wait(k_full, 0, a.wait_ns);
-      for (int s = 0; s < 2; ++s)
-        if (loaded > s) bulk::warp_wait(q_full + 8 * s, ((loaded - 1 - s) >> 1) & 1, a.wait_ns);
+      bulk::warp_wait(kv_full, uint32_t(k) & 1u, a.wait_ns);
+      feed.drain();
+    }
+  } else if (warp == 8) {
+    Place<NS> qs(0), ds(1);  // tiles of the next x and v do^T
+    Place<NS> qk(0), dv(1);  // tiles of the next dk and dv products
+    uint32_t c = 0;          // query tiles so far
+    bool ok = true;
+    // x^T overwrites p^T, v do^T overwrites ds^T: the products execute in the order they are issued
+    auto scores = [&]() {
+      if (!wait(full + 8 * qs.s, qs.phase, a)) return false;
+      mma_rows<DH>(s_at, k_at, qd_at + qs.s * TB);
+      commit(s_full);
+      qs.skip2();
+      return true;
+    };
+    auto products = [&]() {
+      if (!wait(full + 8 * ds.s, ds.phase, a)) return false;
+      mma_rows<DH>(dp_at, v_at, qd_at + ds.s * TB);
+      commit(dp_full);
+      ds.skip2();
+      return true;
+    };
+    for (int k = 0; ok; ++k) {
+      if (!(ok = wait(kv_full, k, a))) break;
+      const int32_t u = ids[k & 3];
+      if (u < 0) break;
+      const Tile x = a.tiles[u / a.kv_heads];
+      int first;
+      const int n = query_tiles(x, a.causal, first) * group;
+      if (!(ok = scores() && products())) break;
+      if (n == 1) commit(kv_free);
+      for (int j = 0; j < n; ++j, ++c) {
+        if (!(ok = wait(p_ready, c, a))) break;
+        tc::fence_after();
+        mma_cols<DH>(dv_at, s_at, s_at + 64, qd_at + dv.s * TB, j != 0);
+        commit(free + 8 * dv.s);
+        dv.skip2();
+        if (j + 1 < n && !(ok = scores())) break;
+        if (!(ok = wait(ds_ready, c, a))) break;
+        tc::fence_after();
+        mma_cols<DH>(dk_at, dp_at, dp_at + 64, qd_at + qk.s * TB, j != 0);
+        commit(free + 8 * qk.s);
+        qk.skip2();
+        if (j + 1 < n && !(ok = products())) break;
+        if (j + 2 == n) commit(kv_free);
+      }
+      if (ok) commit(sums_full);
+    }
+    if (!ok) {
+      commit(drain);
+      wait(drain, 0, a);
     }
   } else {
     const int r = threadIdx.x & 127, half = threadIdx.x >> 7;
-    const int key = x.t * kTile + r;
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t cols = 64 * half;
     const float c = a.scale * kLog2e;
-    // lse (in powers of two) or delta of query r of tile j; queries past the sample's end weigh nothing
-    auto row_value = [&](int j) {
-      const int i = query_tile(j) * kTile + r;
-      const int64_t at = int64_t(query_head(j)) * a.T + x.begin + i;
-      if (half == 0) return i < x.L ? a.lse[at] * kLog2e : INFINITY;
-      return i < x.L ? a.delta[at] : 0.f;
-    };
-    auto put_value = [&](int j, float v) { (half == 0 ? row_lse : row_delta)[j & 1][r] = v; };
-    put_value(0, row_value(0));
+    uint32_t seen = 0;
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      // one barrier a tile: this tile's values are in, and the last tile's are read
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      float next = 0.f;
-      if (j + 1 < n) next = row_value(j + 1);
-      ok = ok && wait(s_full, j, a);
-      if (!ok) continue;  // every warp keeps meeting the barrier
-      tc::fence_after();
-      float p[64];
-      tc::ld32(s_at + lanes + cols, p);
-      tc::ld32(s_at + lanes + cols + 32, p + 32);
-      tc::wait_ld();
-      tc::tie32(p);
-      tc::tie32(p + 32);
-      const float4* ls = reinterpret_cast<const float4*>(&row_lse[j & 1][cols]);
-#pragma unroll
-      for (int i = 0; i < 64; i += 4) {
-        const float4 z = ls[i / 4];
-        tc::fma2(p + i, c, c, -z.x, -z.y);
-        tc::fma2(p + i + 2, c, c, -z.z, -z.w);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) p[i + q] = tc::ex2(p[i + q]);
-      }
-      const int i0 = query_tile(j) * kTile;
-      if (x.t * kTile + kTile > x.uih || (a.causal && i0 < x.t * kTile + kTile)) {
-        // query i0 + cols + i sees this key from `from` on, or only where it is the key's own position
-        const int self = key - i0 - int(cols);
-        const int from = key >= x.uih ? 128 : (a.causal ? self : -1);
-#pragma unroll
-        for (int i = 0; i < 64; ++i) p[i] = (i >= from || i == self) ? p[i] : 0.f;
-      }
-      uint32_t w[32];
-#pragma unroll
-      for (int i = 0; i < 64; i += 2) w[i / 2] = tc::pack2(p[i], p[i + 1]);
-      tc::st32(s_at + lanes + cols, w);
-      tc::wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::arrive(p_ready);
-      if (j + 1 < n) put_value(j + 1, next);
-      ok = wait(dp_full, j, a);
-      if (!ok) continue;
-      tc::fence_after();
-      const float4* dl = reinterpret_cast<const float4*>(&row_delta[j & 1][cols]);
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        float g[32];
-        tc::ld32(dp_at + lanes + cols + 32 * b, g);
+    for (int k = 0; ok; ++k) {
+      if (!(ok = wait(kv_full, k, a))) break;
+      const int32_t u = ids[k & 3];
+      if (u < 0) break;
+      const Tile x = a.tiles[u / a.kv_heads];
+      const int kv_head = u % a.kv_heads;
+      int first;
+      const int nq = query_tiles(x, a.causal, first), n = nq * group;
+      const int key = x.t * kTile + r;
+      // lse (in powers of two) or delta of query r of a tile; queries past the sample's end weigh nothing
+      auto row_value = [&](int tile, int head) {
+        const int i = tile * kTile + r;
+        const int64_t at = int64_t(head) * a.T + x.begin + i;
+        if (half == 0) return i < x.L ? a.lse[at] * kLog2e : INFINITY;
+        return i < x.L ? a.delta[at] : 0.f;
+      };
+      int tile = first, head = kv_head * group;
+      float next = row_value(tile, head);
+      for (int j = 0; j < n; ++j, ++seen) {
+        // this tile's values are in for everyone (and everyone is done with the last tile but one's)
+        (half == 0 ? row_lse : row_delta)[seen & 1][r] = next;
+        __syncwarp();
+        if (lane == 0) tc::arrive(rows_in);
+        const int i0 = tile * kTile;
+        if (++tile == first + nq) tile = first, ++head;
+        if (j + 1 < n) next = row_value(tile, head);
+        if (!(ok = wait(rows_in, seen, a) && wait(s_full, seen, a))) break;
+        tc::fence_after();
+        float p[64];
+        tc::ld32(s_at + lanes + cols, p);
+        tc::ld32(s_at + lanes + cols + 32, p + 32);
         tc::wait_ld();
-        tc::tie32(g);
+        tc::tie32(p);
+        tc::tie32(p + 32);
+        const float4* ls = reinterpret_cast<const float4*>(&row_lse[seen & 1][cols]);
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 z = dl[8 * b + i / 4];
-          tc::add2(g + i, -z.x, -z.y);
-          tc::add2(g + i + 2, -z.z, -z.w);
-          tc::mul2(g + i, p[32 * b + i], p[32 * b + i + 1]);
-          tc::mul2(g + i + 2, p[32 * b + i + 2], p[32 * b + i + 3]);
-          w[16 * b + i / 2] = tc::pack2(g[i], g[i + 1]);
-          w[16 * b + i / 2 + 1] = tc::pack2(g[i + 2], g[i + 3]);
+        for (int i = 0; i < 64; i += 4) {
+          const float4 z = ls[i / 4];
+          tc::fma2(p + i, c, c, -z.x, -z.y);
+          tc::fma2(p + i + 2, c, c, -z.z, -z.w);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) p[i + q] = tc::ex2(p[i + q]);
         }
+        if (x.t * kTile + kTile > x.uih || (a.causal && i0 < x.t * kTile + kTile)) {
+          // query i0 + cols + i sees this key from `from` on, or only where it is the key's own position
+          const int self = key - i0 - int(cols);
+          const int from = key >= x.uih ? 128 : (a.causal ? self : -1);
+#pragma unroll
+          for (int i = 0; i < 64; ++i) p[i] = (i >= from || i == self) ? p[i] : 0.f;
+        }
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) w[i / 2] = tc::pack2(p[i], p[i + 1]);
+        tc::st32(s_at + lanes + cols, w);
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::arrive(p_ready);
+        if (!(ok = wait(dp_full, seen, a))) break;
+        tc::fence_after();
+        const float4* dl = reinterpret_cast<const float4*>(&row_delta[seen & 1][cols]);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          float g[32];
+          tc::ld32(dp_at + lanes + cols + 32 * b, g);
+          tc::wait_ld();
+          tc::tie32(g);
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 z = dl[8 * b + i / 4];
+            tc::add2(g + i, -z.x, -z.y);
+            tc::add2(g + i + 2, -z.z, -z.w);
+            tc::mul2(g + i, p[32 * b + i], p[32 * b + i + 1]);
+            tc::mul2(g + i + 2, p[32 * b + i + 2], p[32 * b + i + 3]);
+            w[16 * b + i / 2] = tc::pack2(g[i], g[i + 1]);
+            w[16 * b + i / 2 + 1] = tc::pack2(g[i + 2], g[i + 3]);
+          }
+        }
+        tc::st32(dp_at + lanes + cols, w);
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::arrive(ds_ready);
       }
-      tc::st32(dp_at + lanes + cols, w);
-      tc::wait_st();
-      tc::fence_before();
-      __syncwarp();
-      if (lane == 0) tc::arrive(ds_ready);
-    }
-    if (ok && wait(fin, 0, a)) {
+      if (!ok || !(ok = wait(sums_full, k, a))) break;
       tc::fence_after();
       const int64_t pos = int64_t(x.begin) + key;
       __nv_bfloat16* to = half == 0 ? a.dv + pos * a.dv_stride : a.dk + pos * a.dk_stride;
@@ -966,7 +1139,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
   __syncthreads();
   if (warp == 8) {
     tc::fence_after();
-    tc::dealloc(tmem_at, 512);
+    tc::dealloc(s_at, 512);
   }
 }
 
@@ -1023,14 +1196,14 @@ fs_status check_rows(const void* p, int64_t stride, int32_t heads, int32_t Dh) {
 int64_t most_tiles(int64_t T, int64_t S) { return T / kTile + (S < T ? S : T); }
 
 struct AttnWs {
-  int32_t* ntiles = nullptr;
+  Plan* plan = nullptr;
   Tile *by_query = nullptr, *by_key = nullptr;
   float* delta = nullptr;
 };
 
 template <class Ws>
 void take_attn(int64_t T, int64_t S, int32_t Hq, Ws& ws, AttnWs& W) {
-  W.ntiles = ws.template take<int32_t>(1);
+  W.plan = ws.template take<Plan>(1);
   W.by_query = ws.template take<Tile>(size_t(most_tiles(T, S)));
   W.by_key = ws.template take<Tile>(size_t(most_tiles(T, S)));
   W.delta = ws.template take<float>(size_t(Hq) * size_t(T));
@@ -1050,6 +1223,23 @@ bool prepare_kernel(K kern, int bytes, int regs, std::atomic<uint64_t>& done) {
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
   done.fetch_or(bit);
   return true;
+}
+
+// Launches a kernel that may start while the one before it in the stream still runs (it waits
+// for that one's end itself, before it reads anything).
+template <class... Params, class... Args>
+void launch_after(void (*kern)(Params...), int64_t grid, int threads, int smem, cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
 std::atomic<uint64_t> g_fwd_ready[2], g_bwd_ready[2][2];
@@ -1093,22 +1283,22 @@ extern "C" fs_status fs_jagged_attn(const void* q, int64_t q_stride, const void*
       !encode(&mv, v, T, int64_t(kv_heads) * head_dim, v_stride))
     return FS_ERR_CUDA;
   AttnArgs a{};
-  a.ntiles = W.ntiles, a.tiles = W.by_query;
+  a.plan = W.plan, a.tiles = W.by_query;
   a.heads = heads, a.kv_heads = kv_heads, a.T = T, a.causal = causal != 0, a.scale = scale;
   a.o = static_cast<__nv_bfloat16*>(out), a.lse = lse, a.err = err;
   a.wait_ns = uint64_t(spin_limit()) * 256u;
   const bool by_head = heads / kv_heads % 2 == 0;  // two heads of one tile share a block, else two tiles of one head
   const int parts = by_head ? heads / 2 : heads;
-  attn_plan_kernel<<<1, kPlanThreads, 0, st>>>(offsets, S, T, cand_len, a.causal, by_head ? 1 : 2, W.ntiles, W.by_query,
+  attn_plan_kernel<<<1, kPlanThreads, 0, st>>>(offsets, S, T, cand_len, a.causal, by_head ? 1 : 2, W.plan, W.by_query,
                                                nullptr, err);
   const int64_t units = most_tiles(T, S) * parts;
-  const unsigned grid = unsigned(units < sm_count() ? units : sm_count());
+  const int64_t grid = units < sm_count() ? units : sm_count();
   if (head_dim == 64) {
     if (!prepare_kernel(attn_fwd_kernel<64>, fwd_smem<64>(), kFwdRegs, g_fwd_ready[0])) return FS_ERR_CUDA;
-    attn_fwd_kernel<64><<<grid, kFwdThreads, fwd_smem<64>(), st>>>(mq, mk, mv, a, parts);
+    launch_after(attn_fwd_kernel<64>, grid, kFwdThreads, fwd_smem<64>(), st, mq, mk, mv, a, parts);
   } else {
     if (!prepare_kernel(attn_fwd_kernel<128>, fwd_smem<128>(), kFwdRegs, g_fwd_ready[1])) return FS_ERR_CUDA;
-    attn_fwd_kernel<128><<<grid, kFwdThreads, fwd_smem<128>(), st>>>(mq, mk, mv, a, parts);
+    launch_after(attn_fwd_kernel<128>, grid, kFwdThreads, fwd_smem<128>(), st, mq, mk, mv, a, parts);
   }
   count_launch(2);
   return launch_status();
@@ -1144,27 +1334,28 @@ extern "C" fs_status fs_jagged_attn_backward(const void* q, int64_t q_stride, co
       !encode(&mdo, dout, T, ow, ow))
     return FS_ERR_CUDA;
   AttnArgs a{};
-  a.ntiles = W.ntiles;
+  a.plan = W.plan;
   a.heads = heads, a.kv_heads = kv_heads, a.T = T, a.causal = causal != 0, a.scale = scale;
   a.out = static_cast<const __nv_bfloat16*>(out), a.dout = static_cast<const __nv_bfloat16*>(dout);
   a.lse = const_cast<float*>(lse), a.delta = W.delta, a.err = err;
   a.dq = static_cast<__nv_bfloat16*>(dq), a.dk = static_cast<__nv_bfloat16*>(dk), a.dv = static_cast<__nv_bfloat16*>(dv);
   a.dq_stride = dq_stride, a.dk_stride = dk_stride, a.dv_stride = dv_stride;
   a.wait_ns = uint64_t(spin_limit()) * 256u;
-  attn_plan_kernel<<<1, kPlanThreads, 0, st>>>(offsets, S, T, cand_len, a.causal, 1, W.ntiles, W.by_query, W.by_key, err);
-  const unsigned gq = unsigned(most_tiles(T, S) * heads), gk = unsigned(most_tiles(T, S) * kv_heads);
+  attn_plan_kernel<<<1, kPlanThreads, 0, st>>>(offsets, S, T, cand_len, a.causal, 1, W.plan, W.by_query, W.by_key, err);
+  const int64_t tiles = most_tiles(T, S), sms = sm_count();
+  const int64_t gq = tiles * heads < sms ? tiles * heads : sms, gk = tiles * kv_heads < sms ? tiles * kv_heads : sms;
   AttnArgs b = a;
   a.tiles = W.by_query, b.tiles = W.by_key;
   if (head_dim == 64) {
     if (!prepare_kernel(attn_dq_kernel<64>, bwd_smem<64>(), 0, g_bwd_ready[0][0])) return FS_ERR_CUDA;
     if (!prepare_kernel(attn_dkv_kernel<64>, bwd_smem<64>(), 0, g_bwd_ready[0][1])) return FS_ERR_CUDA;
-    attn_dq_kernel<64><<<gq, kBwdThreads, bwd_smem<64>(), st>>>(mq, mk, mv, mdo, a);
-    attn_dkv_kernel<64><<<gk, kBwdThreads, bwd_smem<64>(), st>>>(mq, mk, mv, mdo, b);
+    launch_after(attn_dq_kernel<64>, gq, kBwdThreads, bwd_smem<64>(), st, mq, mk, mv, mdo, a);
+    launch_after(attn_dkv_kernel<64>, gk, kBwdThreads, bwd_smem<64>(), st, mq, mk, mv, mdo, b);
   } else {
     if (!prepare_kernel(attn_dq_kernel<128>, bwd_smem<128>(), 0, g_bwd_ready[1][0])) return FS_ERR_CUDA;
     if (!prepare_kernel(attn_dkv_kernel<128>, bwd_smem<128>(), 0, g_bwd_ready[1][1])) return FS_ERR_CUDA;
-    attn_dq_kernel<128><<<gq, kBwdThreads, bwd_smem<128>(), st>>>(mq, mk, mv, mdo, a);
-    attn_dkv_kernel<128><<<gk, kBwdThreads, bwd_smem<128>(), st>>>(mq, mk, mv, mdo, b);
+    launch_after(attn_dq_kernel<128>, gq, kBwdThreads, bwd_smem<128>(), st, mq, mk, mv, mdo, a);
+    launch_after(attn_dkv_kernel<128>, gk, kBwdThreads, bwd_smem<128>(), st, mq, mk, mv, mdo, b);
   }
   count_launch(3);
   return launch_status();
