@@ -195,27 +195,23 @@ struct AttnArgs {
   uint64_t wait_ns;
 };
 
-// Wait of one thread for a barrier's phase, with a limit.  The hand-overs
+// Wait of a whole warp for a barrier's phase, with a limit.  The hand-overs
 // between the warps of a block come every few hundred cycles, so it polls
-// without asking to sleep and looks at the clock only now and then.
-__device__ __forceinline__ bool poll(uint32_t bar, uint32_t phase, const AttnArgs& a) {
-  if (bulk::try_wait(bar, phase & 1u)) return true;
+// without asking to sleep and looks at the clock only now and then.  Every lane polls
+// and a vote decides: beside running products that costs nothing, where one lane's poll, its
+// branch and the broadcast of the answer took 16 to 160 cycles (measured).
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t phase, const AttnArgs& a) {
   uint64_t t0 = 0;
   for (uint32_t polls = 1;; ++polls) {
-    if (bulk::try_wait(bar, phase & 1u)) return true;
+    if (__all_sync(0xffffffffu, bulk::try_wait(bar, phase & 1u))) return true;
     if ((polls & 1023u) == 0) {
       const uint64_t now = bulk::global_ns();
       if (t0 == 0) t0 = now;
-      if (now - t0 > a.wait_ns) break;
+      if (__any_sync(0xffffffffu, now - t0 > a.wait_ns)) break;
     }
   }
-  set_err(a.err, FS_ERR_TIMEOUT);
+  if ((threadIdx.x & 31) == 0) set_err(a.err, FS_ERR_TIMEOUT);
   return false;
-}
-
-// The same for a whole warp.
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t phase, const AttnArgs& a) {
-  return __all_sync(0xffffffffu, poll(bar, phase, a));
 }
 
 // Tile of 128 rows of DH columns from position y of head h, as DH / 64 boxes (one thread).
@@ -387,6 +383,11 @@ struct Place {
     s += 2;
     if (s >= NS) s -= NS, ++phase;
   }
+  static __device__ __forceinline__ Place before(Place p) {  // two items back
+    p.s -= 2;
+    if (p.s < 0) p.s += NS, --p.phase;
+    return p;
+  }
 };
 
 __device__ __forceinline__ void wait_for_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -413,9 +414,10 @@ struct FwdUnit {
   Tile x;
   int head0, head1, row0, row1;  // query head and tile index of each query tile
   int nk0, nk1, own0, own1;      // key tiles of the history, and whether its own tile follows
-  int kv_head, common, n;
-  bool by_head, both;
+  int kv_head, common, n;        // n < 0: no more units
+  int by_head, both;
 
+  FwdUnit() = default;
   __device__ __forceinline__ FwdUnit(const Tile& tile, int part, const AttnArgs& a) : x(tile) {
     const int group = a.heads / a.kv_heads;
     by_head = group % 2 == 0;
@@ -440,6 +442,15 @@ struct FwdUnit {
     if (by_head) return true;
     return i ? j < nk1 || (own1 && j == common + own0) : j < nk0 || (own0 && j == common);
   }
+  // A copy whose fields the compiler knows to be the same in every lane: branches on them are the warp's.
+  __device__ __forceinline__ FwdUnit uniform() const {
+    FwdUnit u = *this;
+    auto same = [](int& v) { v = int(tc::uni(uint32_t(v))); };
+    same(u.x.begin), same(u.x.L), same(u.x.uih);
+    same(u.head0), same(u.head1), same(u.row0), same(u.row1), same(u.nk0), same(u.nk1), same(u.own0), same(u.own1);
+    same(u.kv_head), same(u.common), same(u.n), same(u.by_head), same(u.both);
+    return u;
+  }
 };
 
 template <int DH>
@@ -451,7 +462,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ __align__(8) uint64_t bars[12 + 2 * NS];
   __shared__ uint32_t tmem_at;
-  __shared__ volatile int32_t ids[4];
+  __shared__ FwdUnit given[4];  // units handed over by the loading warp (no reader is two units behind)
   const uint32_t q_at = bulk::smem_addr(smem), kv_at = q_at + 2 * TB;
   const uint32_t bar = bulk::smem_addr(bars);
   const uint32_t q_full = bar, q_free = bar + 8, s_full = bar + 16, p_ready = bar + 32, o_full = bar + 48, tail = bar + 64,
@@ -481,27 +492,34 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
       Taker take{int64_t(a.plan->ntiles) * parts, &a.plan->next[0]};
       bool ok = true;
       int k = 0;
+      int32_t u = take.next();
       for (;; ++k) {
-        const int32_t u = take.next();
-        if (k > 0 && !(ok = feed.mend_all() && wait(q_free, k - 1, a))) break;
-        if (lane == 0) ids[k & 3] = u;
-        if (u < 0) {
-          if (lane == 0) tc::arrive(q_full);
-          break;
+        FwdUnit f;
+        f.n = -1;
+        if (u >= 0) f = FwdUnit(a.tiles[u / parts], u % parts, a).uniform();
+        if (lane == 0) given[k & 3] = f;
+        if (f.n < 0) break;
+        // the first key and value tile need only a slot, the query tiles the end of the last unit's scores
+        auto put = [&](int j) {
+          const int at = f.key_tile(j) * kTile;
+          return feed.put(&mk, f.kv_head, f.x.begin + at, f.x.L - at, false) &&
+                 feed.put(&mv, f.kv_head, f.x.begin + at, f.x.L - at, true);
+        };
+        if (!(ok = put(0))) break;
+        if (k > 0) {
+          if (!__all_sync(0xffffffffu, bulk::try_wait(q_free, uint32_t(k - 1) & 1u)) && !(ok = feed.mend_all())) break;
+          if (!(ok = wait(q_free, k - 1, a))) break;
         }
-        const FwdUnit f(a.tiles[u / parts], u % parts, a);
         if (lane == 0) {
           bulk::arrive_expect_tx(q_full, f.both ? 2 * TB : TB);
           load_tile<DH>(q_at, &mq, f.head0, f.x.begin + f.row0 * kTile, q_full);
           if (f.both) load_tile<DH>(q_at + TB, &mq, f.head1, f.x.begin + f.row1 * kTile, q_full);
         }
-        for (int j = 0; ok && j < f.n; ++j) {
-          const int at = f.key_tile(j) * kTile;
-          ok = feed.put(&mk, f.kv_head, f.x.begin + at, f.x.L - at, false) &&
-               feed.put(&mv, f.kv_head, f.x.begin + at, f.x.L - at, true);
-        }
+        u = take.next();
+        for (int j = 1; ok && j < f.n; ++j) ok = put(j);
         if (!ok) break;
       }
+      if (ok && (ok = feed.mend_all() && (k == 0 || wait(q_free, k - 1, a))) && lane == 0) tc::arrive(q_full);
       if (!ok) {
         bulk::warp_wait(q_full, uint32_t(k) & 1u, a.wait_ns);
         feed.drain();
@@ -514,41 +532,43 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
       bool ok = true;
       for (int k = 0; ok; ++k) {
         if (!(ok = wait(q_full, k, a))) break;
-        const int32_t u = ids[k & 3];
-        if (u < 0) break;
-        const FwdUnit f(a.tiles[u / parts], u % parts, a);
+        const FwdUnit f = given[k & 3].uniform();
+        if (f.n < 0) break;
         bool acc[2] = {false, false};
+        if (!(ok = wait(full + 8 * ks.s, ks.phase, a))) break;
         for (int j = 0; j <= f.n; ++j) {
-          if (j > 0 && !(ok = wait(full + 8 * vs.s, vs.phase, a))) break;
-          if (j < f.n && !(ok = wait(full + 8 * ks.s, ks.phase, a))) break;
+          const Place<NS> v = vs, key = ks;
+          if (j > 0) vs.skip2();
+          ks.skip2();
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
+            // while the first tile's products run: this step's value tile is there for both; the next
+            // step's tiles are looked for before the second tile's
+            if (i == 1 && j < f.n) {
+              if (!(ok = wait(full + 8 * vs.s, vs.phase, a))) break;
+              if (j + 1 < f.n && !(ok = wait(full + 8 * ks.s, ks.phase, a))) break;
+            }
             if (i == 1 && !f.both) continue;
             if (j > 0 && f.meets(i, j - 1)) {
               if (!(ok = wait(p_ready + 8 * i, done[i], a))) break;
               ++done[i];
               tc::fence_after();
-              mma_cols<DH>(o_at + DH * i, s_at + 128 * i, s_at + 128 * i + 32, kv_at + vs.s * TB, acc[i]);
+              mma_cols<DH>(o_at + DH * i, s_at + 128 * i, s_at + 128 * i + 32, kv_at + v.s * TB, acc[i]);
               acc[i] = true;
             }
             if (j < f.n && f.meets(i, j)) {
               // x overwrites p: the products execute in the order they are issued
-              mma_rows<DH>(s_at + 128 * i, q_at + i * TB, kv_at + ks.s * TB);
+              mma_rows<DH>(s_at + 128 * i, q_at + i * TB, kv_at + key.s * TB);
               commit(s_full + 8 * i);
             }
           }
           if (!ok) break;
-          if (j > 0) {
-            commit(free + 8 * vs.s);
-            vs.skip2();
-          }
-          if (j < f.n) {
-            commit(free + 8 * ks.s);
-            ks.skip2();
-          }
+          if (j > 0) commit(free + 8 * v.s);
+          if (j < f.n) commit(free + 8 * key.s);
           if (j == f.n - 1) commit(q_free);
           if (j == f.n) commit(o_full);
         }
+        ks = Place<NS>::before(ks);  // (the last step has no key tile)
       }
       if (!ok) {
         commit(drain);
@@ -566,11 +586,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!(ok = wait(q_full, k, a))) break;
-      const int32_t u = ids[k & 3];
-      if (u < 0) break;
+      const FwdUnit f = given[k & 3].uniform();
+      if (f.n < 0) break;
       __syncwarp();
       if (lane == 0) tc::arrive(q_free);  // (a warpgroup without work in this unit keeps step with the others)
-      const FwdUnit f(a.tiles[u / parts], u % parts, a);
       if (i == 1 && !f.both) {
         if (!(ok = wait(o_full, k, a))) break;
         continue;
