@@ -47,6 +47,8 @@ struct Tile {
   int32_t begin;  // first position of the sample
   int32_t L, uih;
   int32_t t;      // tile index inside the sample
+  int32_t part;   // which half of a key tile's work (only where split >= 0)
+  int32_t split;  // number of the halved key tile, -1: in one piece
 };
 
 // Key tiles that query tile t meets: the first n (those of the history up to
@@ -73,9 +75,13 @@ __device__ __forceinline__ int query_tiles(const Tile& x, bool causal, int& firs
 constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32, kBuckets = 1024;
 
 struct Plan {
-  int32_t ntiles;
-  int32_t next[2];  // units handed out beyond the first of each block: queries, keys
+  int32_t ntiles[2];  // entries of the two lists: queries, keys
+  int32_t next[2];    // units handed out beyond the first of each block
 };
+
+// At most this many (key tile, key/value head) units are cut in half: each takes over half of
+// an SM's share of all the work.
+constexpr int64_t most_split(int64_t sms) { return 2 * sms; }
 
 // Lists the tiles of all samples twice, by descending number of key tiles (for
 // queries; an entry stands for `span` neighbouring tiles, and its t counts such
@@ -83,25 +89,53 @@ struct Plan {
 // counting sort over the tile counts by one block.  The order among equals
 // does not matter to any result.  A warp takes up to 32 samples at a time and
 // spreads their tiles over its lanes.
+// A key tile whose units (one per key/value head, over `group` query heads) each take more than half of
+// an SM's share of the whole work is listed as two halves: in a batch with a few long samples
+// one such unit would otherwise set the time.
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const int64_t* __restrict__ offsets, int64_t S, int64_t T,
                                                                  const int32_t* __restrict__ cand, bool causal,
-                                                                 int span, Plan* plan, Tile* by_query, Tile* by_key,
+                                                                 int span, int kv_heads, int group, int sms, Plan* plan,
+                                                                 Tile* by_query, Tile* by_key, int32_t* flags,
                                                                  int32_t* err) {
   __shared__ int32_t hist[2][kBuckets];
   __shared__ int32_t scan[32];
+  __shared__ unsigned long long work;
+  __shared__ int32_t nsplit;
   asm volatile("griddepcontrol.launch_dependents;");
   for (int i = threadIdx.x; i < 2 * kBuckets; i += kPlanThreads) (&hist[0][0])[i] = 0;
   if (threadIdx.x < 2) plan->next[threadIdx.x] = 0;
+  if (threadIdx.x == 0) work = 0, nsplit = 0;
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = span * kTile;
-  const int64_t share = (S + kPlanWarps - 1) / kPlanWarps;
-  const int group = share < 32 ? int(share) : 32;  // samples a warp takes at a time
   auto bucket = [](int cost) { return kBuckets - min(cost, kBuckets); };  // most work first
+  // Query tiles that all key tiles of a sample meet.
+  auto tiles_met = [&](int64_t L, int64_t uih) {
+    const int64_t all = (L + kTile - 1) / kTile, seen = (uih + kTile - 1) / kTile;
+    return (causal ? seen * all - seen * (seen - 1) / 2 : seen * all) + (all - seen);
+  };
+  if (by_key) {
+    unsigned long long mine = 0;
+    for (int64_t s = threadIdx.x; s < S; s += kPlanThreads) {
+      const int64_t b = offsets[s], e = offsets[s + 1];
+      if (b < 0 || e < b || e > T) continue;
+      int64_t c = cand ? cand[s] : 0;
+      c = c < 0 ? 0 : (c > e - b ? e - b : c);
+      mine += (unsigned long long)(tiles_met(e - b, e - b - c));
+    }
+    if (mine) atomicAdd(&work, mine);
+    for (int64_t i = threadIdx.x; i < most_split(sms) * 8; i += kPlanThreads) flags[i] = 0;
+    __syncthreads();
+  }
+  const int64_t share = (S + kPlanWarps - 1) / kPlanWarps;
+  const int take = share < 32 ? int(share) : 32;  // samples a warp takes at a time
+  // half of an SM's share, in query tiles of one unit's `group` heads
+  const int64_t half = by_key ? int64_t(work) * kv_heads / (2 * sms) : 0;
+  auto cut = [&](int nq) { return by_key && nq * group > 1 && nq > half; };
   auto each = [&](bool report, auto f) {
-    for (int64_t s0 = int64_t(warp) * group; s0 < S; s0 += int64_t(kPlanWarps) * group) {
+    for (int64_t s0 = int64_t(warp) * take; s0 < S; s0 += int64_t(kPlanWarps) * take) {
       int32_t begin = 0, L = 0, c = 0;
-      if (lane < group && s0 + lane < S) {
+      if (lane < take && s0 + lane < S) {
         const int64_t b = offsets[s0 + lane], e = offsets[s0 + lane + 1];
         if (b < 0 || e < b || e > T) {
           if (report) set_err(err, FS_ERR_BAD_OFFSETS);
@@ -130,7 +164,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const int64_t* 
         for (int o = 16; o > 0; o >>= 1)
           if (__shfl_sync(0xffffffffu, upto, (who + o - 1) & 31) <= i) who += o;
         who &= 31;
-        Tile x{__shfl_sync(0xffffffffu, begin, who), __shfl_sync(0xffffffffu, L, who), 0, 0};
+        Tile x{__shfl_sync(0xffffffffu, begin, who), __shfl_sync(0xffffffffu, L, who), 0, 0, 0, -1};
         x.uih = x.L - __shfl_sync(0xffffffffu, c, who);
         x.t = i - (__shfl_sync(0xffffffffu, upto, who) - __shfl_sync(0xffffffffu, mine, who));
         if (i < all) {
@@ -138,16 +172,16 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const int64_t* 
           Tile last = x;  // the entry's last tile has the most key tiles
           last.t = min(x.t * span + span - 1, (x.L - 1) / kTile);
           const int nk = key_tiles(last, causal, own) + own;
-          f(x, bucket(nk), bucket(query_tiles(x, causal, first)));
+          f(x, nk, query_tiles(x, causal, first));
         }
         __syncwarp();
       }
     }
   };
   int64_t total = 0;
-  each(true, [&](const Tile&, int bq, int bk) {
-    atomicAdd(&hist[0][bq], 1);
-    if (by_key) atomicAdd(&hist[1][bk], 1);
+  each(true, [&](const Tile&, int nk, int nq) {
+    atomicAdd(&hist[0][bucket(nk)], 1);
+    if (by_key) atomicAdd(&hist[1][bucket(cut(nq) ? (nq + 1) / 2 : nq)], cut(nq) ? 2 : 1);
   });
   __syncthreads();
   for (int w = 0; w < (by_key ? 2 : 1); ++w) {
@@ -155,7 +189,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const int64_t* 
     const int32_t mine = hist[w][threadIdx.x];
     const int32_t at = block_exclusive_scan<int32_t>(mine, scan, &n);
     hist[w][threadIdx.x] = at;
-    total = n;
+    if (w == 0) total = n;
+    if (threadIdx.x == 0) plan->ntiles[w] = n;
   }
   __syncthreads();
   // Offsets that are not in order can describe more tiles than the lists hold:
@@ -164,14 +199,23 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const int64_t* 
   if (total > most) {
     if (threadIdx.x == 0) {
       set_err(err, FS_ERR_BAD_OFFSETS);
-      plan->ntiles = 0;
+      plan->ntiles[0] = plan->ntiles[1] = 0;
     }
     return;
   }
-  if (threadIdx.x == 0) plan->ntiles = int32_t(total);
-  each(false, [&](const Tile& x, int bq, int bk) {
-    by_query[atomicAdd(&hist[0][bq], 1)] = x;
-    if (by_key) by_key[atomicAdd(&hist[1][bk], 1)] = x;
+  each(false, [&](Tile x, int nk, int nq) {
+    by_query[atomicAdd(&hist[0][bucket(nk)], 1)] = x;
+    if (by_key) {
+      if (cut(nq)) {
+        const int32_t at = atomicAdd(&hist[1][bucket((nq + 1) / 2)], 2);
+        x.split = atomicAdd(&nsplit, 1);
+        by_key[at] = x;
+        x.part = 1;
+        by_key[at + 1] = x;
+      } else {
+        by_key[atomicAdd(&hist[1][bucket(nq)], 1)] = x;
+      }
+    }
   });
 }
 
@@ -185,10 +229,10 @@ struct AttnArgs {
   bool causal;
   float scale;
   __nv_bfloat16* o;           // forward: out
-  const __nv_bfloat16* out;   // backward: out and dout
-  const __nv_bfloat16* dout;
   float* lse;
   float* delta;               // [heads, T]: written by the dq kernel, read by the dk / dv kernel
+  float* partial;             // sums of the halves of key tiles
+  int32_t* flags;             // and who of the two came first, for each warp of a unit
   __nv_bfloat16 *dq, *dk, *dv;
   int64_t dq_stride, dk_stride, dv_stride;
   int32_t* err;
@@ -357,17 +401,38 @@ __device__ __forceinline__ void commit(uint32_t bar) {
   if ((threadIdx.x & 31) == 0) tc::commit(bar);
 }
 
-// 32 fp32 columns, scaled, as bf16 to 64 contiguous bytes.
-__device__ __forceinline__ void store32(__nv_bfloat16* p, const float* x, float f) {
+// 32 fp32 columns of each lane's row, scaled, as bf16: `to` is column 0 of the
+// warp's first row, rows are `stride` elements apart, the first `live` of the 32
+// exist.  Four neighbouring lanes exchange 16-byte pieces (a 4 x 4 transpose by shuffles), so that a
+// store writes 64 bytes of 8 rows instead of 16 bytes of 32 (an epilogue of 128 rows of
+// 256 bytes took 4000 to 6000 cycles that way).
+__device__ __forceinline__ void store32(__nv_bfloat16* to, int64_t stride, int live, const float* x, float f) {
+  const int lane = threadIdx.x & 31, s = lane & 3, q = lane >> 2;
+  uint32_t v[4][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint4 v;
-    v.x = tc::pack2(x[8 * i] * f, x[8 * i + 1] * f);
-    v.y = tc::pack2(x[8 * i + 2] * f, x[8 * i + 3] * f);
-    v.z = tc::pack2(x[8 * i + 4] * f, x[8 * i + 5] * f);
-    v.w = tc::pack2(x[8 * i + 6] * f, x[8 * i + 7] * f);
-    reinterpret_cast<uint4*>(p)[i] = v;
-  }
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) v[c][w] = tc::pack2(x[8 * c + 2 * w] * f, x[8 * c + 2 * w + 1] * f);
+#pragma unroll
+  for (int c = 0; c < 4; c += 2)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, (s & 1) ? v[c][w] : v[c + 1][w], 1);
+      if (s & 1) v[c][w] = got;
+      else v[c + 1][w] = got;
+    }
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, (s & 2) ? v[c][w] : v[c + 2][w], 2);
+      if (s & 2) v[c][w] = got;
+      else v[c + 2][w] = got;
+    }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (4 * q + j < live)
+      *reinterpret_cast<uint4*>(to + int64_t(4 * q + j) * stride + 8 * s) = make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
 }
 
 template <int DH>
@@ -379,14 +444,13 @@ struct Place {
   int s;
   uint32_t phase = 0;
   __device__ __forceinline__ explicit Place(int first) : s(first) {}
-  __device__ __forceinline__ void skip2() {  // two items further on
-    s += 2;
+  __device__ __forceinline__ void skip(int k) {  // k <= NS items further on
+    s += k;
     if (s >= NS) s -= NS, ++phase;
   }
-  static __device__ __forceinline__ Place before(Place p) {  // two items back
-    p.s -= 2;
-    if (p.s < 0) p.s += NS, --p.phase;
-    return p;
+  __device__ __forceinline__ void back(int k) {
+    s -= k;
+    if (s < 0) s += NS, --phase;
   }
 };
 
@@ -489,7 +553,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 9) {
       Feeder<DH, NS> feed(smem + 2 * TB, full, free, tail, a);
-      Taker take{int64_t(a.plan->ntiles) * parts, &a.plan->next[0]};
+      Taker take{int64_t(a.plan->ntiles[0]) * parts, &a.plan->next[0]};
       bool ok = true;
       int k = 0;
       int32_t u = take.next();
@@ -506,10 +570,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
                  feed.put(&mv, f.kv_head, f.x.begin + at, f.x.L - at, true);
         };
         if (!(ok = put(0))) break;
-        if (k > 0) {
-          if (!__all_sync(0xffffffffu, bulk::try_wait(q_free, uint32_t(k - 1) & 1u)) && !(ok = feed.mend_all())) break;
-          if (!(ok = wait(q_free, k - 1, a))) break;
-        }
+        if (k > 0 && !(ok = wait(q_free, k - 1, a))) break;
         if (lane == 0) {
           bulk::arrive_expect_tx(q_full, f.both ? 2 * TB : TB);
           load_tile<DH>(q_at, &mq, f.head0, f.x.begin + f.row0 * kTile, q_full);
@@ -517,7 +578,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
         }
         u = take.next();
         for (int j = 1; ok && j < f.n; ++j) ok = put(j);
-        if (!ok) break;
+        if (!ok || !(ok = feed.mend_all())) break;
       }
       if (ok && (ok = feed.mend_all() && (k == 0 || wait(q_free, k - 1, a))) && lane == 0) tc::arrive(q_full);
       if (!ok) {
@@ -538,16 +599,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
         if (!(ok = wait(full + 8 * ks.s, ks.phase, a))) break;
         for (int j = 0; j <= f.n; ++j) {
           const Place<NS> v = vs, key = ks;
-          if (j > 0) vs.skip2();
-          ks.skip2();
+          if (j > 0) vs.skip(2);
+          ks.skip(2);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             // while the first tile's products run: this step's value tile is there for both; the next
             // step's tiles are looked for before the second tile's
-            if (i == 1 && j < f.n) {
-              if (!(ok = wait(full + 8 * vs.s, vs.phase, a))) break;
-              if (j + 1 < f.n && !(ok = wait(full + 8 * ks.s, ks.phase, a))) break;
-            }
+            if (i == 1 && j + 1 < f.n && !(ok = wait(full + 8 * vs.s, vs.phase, a) && wait(full + 8 * ks.s, ks.phase, a)))
+              break;
+            if (i == 0 && j == f.n && !(ok = wait(full + 8 * v.s, v.phase, a))) break;  // (the last may be mended)
             if (i == 1 && !f.both) continue;
             if (j > 0 && f.meets(i, j - 1)) {
               if (!(ok = wait(p_ready + 8 * i, done[i], a))) break;
@@ -568,7 +628,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
           if (j == f.n - 1) commit(q_free);
           if (j == f.n) commit(o_full);
         }
-        ks = Place<NS>::before(ks);  // (the last step has no key tile)
+        ks.back(2);  // (the last step has no key tile)
       }
       if (!ok) {
         commit(drain);
@@ -680,7 +740,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
         tc::ld32(acc_at + 32 * b, o);
         tc::wait_ld();
         tc::tie32(o);
-        if (row < f.x.L) store32(a.o + (pos * a.heads + head) * DH + 32 * b, o, inv);
+        store32(a.o + ((pos - lane) * a.heads + head) * DH + 32 * b, int64_t(a.heads) * DH, f.x.L - row + lane, o, inv);
       }
       if (row < f.x.L) a.lse[int64_t(head) * a.T + pos] = (m * c + log2f(l)) * (1.f / kLog2e);
       tc::fence_before();
@@ -699,20 +759,48 @@ constexpr int kBwdThreads = 320;  // eight warps for the elementwise part, one f
 template <int DH> constexpr int bwd_slots() { return DH == 64 ? 10 : 5; }
 template <int DH> constexpr int bwd_smem() { return tile_bytes<DH>() * (2 + bwd_slots<DH>()); }
 
+__device__ __forceinline__ Tile uniform_tile(Tile x) {
+  auto same = [](int& v) { v = int(tc::uni(uint32_t(v))); };
+  same(x.begin), same(x.L), same(x.uih), same(x.t), same(x.part), same(x.split);
+  return x;
+}
+
 // dq of one query tile and head a unit.  A thread holds one query row and 64 of
 // the 128 keys.  Per key tile: x = q k^T and do v^T into 128 columns each; p = exp(x - lse)
 // stays in registers and frees x, so the next tile's x is computed while
 // ds = p * (do v^T - delta) is formed; ds (bf16) goes over do v^T and multiplies k.
+// The unit's rows of out come through the ring in front of its keys, for delta.
+struct DqUnit {
+  Tile x;
+  int head, kv_head, nk, n;  // n < 0: no more units
+  DqUnit() = default;
+  __device__ __forceinline__ DqUnit(const Tile& tile, int h, const AttnArgs& a) : x(tile), head(h) {
+    kv_head = head / (a.heads / a.kv_heads);
+    int own;
+    nk = key_tiles(x, a.causal, own);
+    n = nk + own;
+  }
+  __device__ __forceinline__ int key_tile(int j) const { return j < nk ? j : x.t; }
+  __device__ __forceinline__ DqUnit uniform() const {
+    DqUnit u = *this;
+    auto same = [](int& v) { v = int(tc::uni(uint32_t(v))); };
+    u.x = uniform_tile(x);
+    same(u.head), same(u.kv_head), same(u.nk), same(u.n);
+    return u;
+  }
+};
+
 template <int DH>
 __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_constant__ CUtensorMap mq,
                                                                  const __grid_constant__ CUtensorMap mk,
                                                                  const __grid_constant__ CUtensorMap mv,
+                                                                 const __grid_constant__ CUtensorMap mo,
                                                                  const __grid_constant__ CUtensorMap mdo, AttnArgs a) {
   constexpr int TB = tile_bytes<DH>(), NS = bwd_slots<DH>();
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ __align__(8) uint64_t bars[11 + 2 * NS];
   __shared__ uint32_t tmem_at;
-  __shared__ volatile int32_t ids[4];
+  __shared__ DqUnit given[4];
   __shared__ float half_delta[2][kTile];
   const uint32_t q_at = bulk::smem_addr(smem), do_at = q_at + TB, kv_at = do_at + TB;
   const uint32_t bar = bulk::smem_addr(bars);
@@ -722,50 +810,51 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
   const int warp = int(tc::uni(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (warp == 8) {
     if (lane == 0) {
-      for (int i = 0; i < 11 + 2 * NS; ++i) bulk::mbar_init(bar + 8 * i, i >= 4 && i <= 6 ? 8 : 1);
+      for (int i = 0; i < 11 + 2 * NS; ++i) bulk::mbar_init(bar + 8 * i, i == 1 ? 2 : (i >= 4 && i <= 6 ? 8 : 1));
       bulk::fence_init();
     }
     __syncwarp();
     tc::alloc(&tmem_at, 512);
     tc::fence_before();
   } else if (warp == 9 && lane == 0) {
-    tc::prefetch_map(&mq), tc::prefetch_map(&mk), tc::prefetch_map(&mv), tc::prefetch_map(&mdo);
+    tc::prefetch_map(&mq), tc::prefetch_map(&mk), tc::prefetch_map(&mv), tc::prefetch_map(&mo), tc::prefetch_map(&mdo);
   }
   __syncthreads();
   tc::fence_after();
   wait_for_launch();
   let_next_launch();
   const uint32_t s_at = tc::uni(tmem_at), dp_at = s_at + 128, dq_at = s_at + 256;
-  const int group = a.heads / a.kv_heads;
 
   if (warp == 9) {
     Feeder<DH, NS> feed(smem + 2 * TB, full, free, tail, a);
-    Taker take{int64_t(a.plan->ntiles) * a.heads, &a.plan->next[0]};
+    Taker take{int64_t(a.plan->ntiles[0]) * a.heads, &a.plan->next[0]};
     bool ok = true;
     int k = 0;
+    int32_t u = take.next();
     for (;; ++k) {
-      const int32_t u = take.next();
-      if (k > 0 && !(ok = feed.mend_all() && wait(q_free, k - 1, a))) break;
-      if (lane == 0) ids[k & 3] = u;
-      if (u < 0) {
-        if (lane == 0) tc::arrive(q_full);
-        break;
-      }
-      const Tile x = a.tiles[u / a.heads];
-      const int head = u % a.heads, kv_head = head / group;
-      int own;
-      const int nk = key_tiles(x, a.causal, own), n = nk + own;
+      DqUnit f;
+      f.n = -1;
+      if (u >= 0) f = DqUnit(a.tiles[u / a.heads], u % a.heads, a).uniform();
+      if (lane == 0) given[k & 3] = f;
+      if (f.n < 0) break;
+      auto put = [&](int j) {
+        const int at = f.key_tile(j) * kTile;
+        return feed.put(&mk, f.kv_head, f.x.begin + at, f.x.L - at, true) &&
+               feed.put(&mv, f.kv_head, f.x.begin + at, f.x.L - at, false);
+      };
+      const int at = f.x.begin + f.x.t * kTile;
+      if (!(ok = feed.put(&mo, f.head, at, kTile, false) && put(0))) break;
+      if (k > 0 && !(ok = wait(q_free, k - 1, a))) break;
       if (lane == 0) {
         bulk::arrive_expect_tx(q_full, 2 * TB);
-        load_tile<DH>(q_at, &mq, head, x.begin + x.t * kTile, q_full);
-        load_tile<DH>(do_at, &mdo, head, x.begin + x.t * kTile, q_full);
+        load_tile<DH>(q_at, &mq, f.head, at, q_full);
+        load_tile<DH>(do_at, &mdo, f.head, at, q_full);
       }
-      for (int j = 0; ok && j < n; ++j) {
-        const int at = (j < nk ? j : x.t) * kTile;
-        ok = feed.put(&mk, kv_head, x.begin + at, x.L - at, true) && feed.put(&mv, kv_head, x.begin + at, x.L - at, false);
-      }
-      if (!ok) break;
+      u = take.next();
+      for (int j = 1; ok && j < f.n; ++j) ok = put(j);
+      if (!ok || !(ok = feed.mend_all())) break;
     }
+    if (ok && (ok = k == 0 || wait(q_free, k - 1, a)) && lane == 0) tc::arrive(q_full);
     if (!ok) {
       bulk::warp_wait(q_full, uint32_t(k) & 1u, a.wait_ns);
       feed.drain();
@@ -779,35 +868,35 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
       tc::fence_after();
       mma_rows<DH>(s_at, q_at, kv_at + ks.s * TB);
       commit(s_full);
-      ks.skip2();
+      ks.skip(2);
       return true;
     };
     auto products = [&]() {  // do v^T of the next value tile, over ds: the products execute in the order they are issued
-      if (!wait(full + 8 * vs.s, vs.phase, a)) return false;
       mma_rows<DH>(dp_at, do_at, kv_at + vs.s * TB);
       commit(dp_full);
       commit(free + 8 * vs.s);
-      vs.skip2();
-      return true;
+      vs.skip(2);
     };
     for (int k = 0; ok; ++k) {
       if (!(ok = wait(q_full, k, a))) break;
-      const int32_t u = ids[k & 3];
-      if (u < 0) break;
-      const Tile x = a.tiles[u / a.heads];
-      int own;
-      const int nk = key_tiles(x, a.causal, own), n = nk + own;
-      if (!(ok = scores() && products())) break;
+      const int n = int(tc::uni(uint32_t(given[k & 3].n)));
+      if (n < 0) break;
+      ks.skip(1), vs.skip(1), kq.skip(1);  // (the tile of out)
+      if (!(ok = scores() && wait(full + 8 * vs.s, vs.phase, a))) break;
+      products();
       for (int j = 0; j < n; ++j) {
         ++c;
-        if (j + 1 < n && !(ok = scores())) break;
-        if (j + 1 == n) commit(q_free);
+        if (j + 1 < n) {
+          if (!(ok = scores() && wait(full + 8 * vs.s, vs.phase, a))) break;
+        } else {
+          commit(q_free);
+        }
         if (!(ok = wait(ds_ready, c - 1, a))) break;
         tc::fence_after();
         mma_cols<DH>(dq_at, dp_at, dp_at + 64, kv_at + kq.s * TB, j != 0);
         commit(free + 8 * kq.s);
-        kq.skip2();
-        if (j + 1 < n && !(ok = products())) break;
+        kq.skip(2);
+        if (j + 1 < n) products();
       }
       if (ok) commit(dq_full);
     }
@@ -820,43 +909,48 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t cols = 64 * half;
     const float c = a.scale * kLog2e;
-    uint32_t seen = 0;
+    uint32_t seen = 0, item = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!(ok = wait(q_full, k, a))) break;
-      const int32_t u = ids[k & 3];
-      if (u < 0) break;
-      const Tile x = a.tiles[u / a.heads];
-      const int head = u % a.heads;
-      int own;
-      const int nk = key_tiles(x, a.causal, own), n = nk + own;
+      const DqUnit f = given[k & 3].uniform();
+      if (f.n < 0) break;
+      const Tile& x = f.x;
       const int row = x.t * kTile + r;
       const bool live = row < x.L;
       const int64_t pos = int64_t(x.begin) + row;
-      // delta = dout.out of the row, half of the columns each
-      float d = 0.f, lse2 = 0.f;
-      if (live) {
-        lse2 = a.lse[int64_t(head) * a.T + pos] * kLog2e;
-        const uint4* po = reinterpret_cast<const uint4*>(a.out + (pos * a.heads + head) * DH + half * (DH / 2));
-        const uint4* pg = reinterpret_cast<const uint4*>(a.dout + (pos * a.heads + head) * DH + half * (DH / 2));
+      const float lse2 = live ? a.lse[int64_t(f.head) * a.T + pos] * kLog2e : 0.f;
+      // delta = dout.out of the row, half of the columns each, from the loaded tiles (16-byte pieces of
+      // a row lie swizzled: piece c of row r at c ^ (r & 7))
+      const int o_slot = int(item % NS);
+      if (!(ok = wait(full + 8 * o_slot, item / NS, a))) break;
+      item += 1 + 2 * uint32_t(f.n);
+      float d = 0.f;
 #pragma unroll
-        for (int i = 0; i < DH / 16; ++i) {
-          const uint4 v = __ldg(po + i), w = __ldg(pg + i);
-          const uint32_t vv[4] = {v.x, v.y, v.z, v.w}, ww[4] = {w.x, w.y, w.z, w.w};
+      for (int i = 0; i < DH / 16; ++i) {
+        const int piece = half * (DH / 16) + i;
+        const int at = (piece / 8) * kBox + r * 128 + (((piece % 8) ^ (r & 7)) * 16);
+        const uint4 v = *reinterpret_cast<const uint4*>(smem + (2 + o_slot) * TB + at);
+        const uint4 w = *reinterpret_cast<const uint4*>(smem + TB + at);
+        const uint32_t vv[4] = {v.x, v.y, v.z, v.w}, ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            d = fmaf(__uint_as_float(vv[q] << 16), __uint_as_float(ww[q] << 16), d);
-            d = fmaf(__uint_as_float(vv[q] & 0xFFFF0000u), __uint_as_float(ww[q] & 0xFFFF0000u), d);
-          }
+        for (int q = 0; q < 4; ++q) {
+          d = fmaf(__uint_as_float(vv[q] << 16), __uint_as_float(ww[q] << 16), d);
+          d = fmaf(__uint_as_float(vv[q] & 0xFFFF0000u), __uint_as_float(ww[q] & 0xFFFF0000u), d);
         }
       }
       half_delta[half][r] = d;
       __syncwarp();
       if (lane == 0) tc::arrive(delta_in);
       if (!(ok = wait(delta_in, k, a))) break;
+      if (threadIdx.x == 0) {  // everyone has read the tiles of out and dout
+        tc::arrive(free + 8 * o_slot);
+        tc::arrive(q_free);
+      }
+      __syncwarp();
       const float delta = half_delta[0][r] + half_delta[1][r];
-      if (live && half == 0) a.delta[int64_t(head) * a.T + pos] = delta;
-      for (int j = 0; j < n; ++j, ++seen) {
+      if (live && half == 0) a.delta[int64_t(f.head) * a.T + pos] = delta;
+      for (int j = 0; j < f.n; ++j, ++seen) {
         if (!(ok = wait(s_full, seen, a))) break;
         tc::fence_after();
         float p[64];
@@ -868,7 +962,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
         tc::fence_before();
         __syncwarp();
         if (lane == 0) tc::arrive(s_read);
-        const int t0 = (j < nk ? j : x.t) * kTile, k0 = t0 + int(cols);
+        const int t0 = f.key_tile(j) * kTile, k0 = t0 + int(cols);
         const bool masked = t0 + kTile > x.uih || (a.causal && t0 + kTile > x.t * kTile);
         const int lim = (a.causal ? min(x.uih, row + 1) : x.uih) - k0, self = row - k0;
 #pragma unroll
@@ -913,7 +1007,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
         tc::ld32(dq_at + lanes + col, g);
         tc::wait_ld();
         tc::tie32(g);
-        if (live) store32(a.dq + pos * a.dq_stride + head * DH + col, g, a.scale);
+        store32(a.dq + (pos - lane) * a.dq_stride + f.head * DH + col, a.dq_stride, x.L - row + lane, g, a.scale);
       }
       tc::fence_before();
     }
@@ -926,10 +1020,42 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
 }
 
 // dk and dv of one key tile and key/value head a unit, over the query heads that
-// share it and the query tiles that see it.  A thread holds one key and 64 of
+// share it and the query tiles that see it, or over half of those.  A thread holds one key and 64 of
 // the 128 queries (everything transposed: x^T = k q^T, v do^T).  p^T (bf16)
 // goes over x^T and multiplies do, then the next x^T is computed while
 // ds^T = p^T * (v do^T - delta) is formed; ds^T goes over v do^T and multiplies q.
+// Of two halves each leaves its sums in fp32, and the one that comes second
+// adds the other's: two terms, so the order does not show.
+struct DkvUnit {
+  Tile x;
+  int kv_head, first, nq, begin, n;  // query tiles [begin, begin + n) of the list (head by head, nq each); n < 0: no more
+  DkvUnit() = default;
+  __device__ __forceinline__ DkvUnit(const Tile& tile, int h, const AttnArgs& a) : x(tile), kv_head(h) {
+    nq = query_tiles(x, a.causal, first);
+    const int all = nq * (a.heads / a.kv_heads), cut = (all + 1) / 2;
+    begin = x.split >= 0 && x.part ? cut : 0;
+    n = x.split >= 0 ? (x.part ? all - cut : cut) : all;
+  }
+  __device__ __forceinline__ DkvUnit uniform() const {
+    DkvUnit u = *this;
+    auto same = [](int& v) { v = int(tc::uni(uint32_t(v))); };
+    u.x = uniform_tile(x);
+    same(u.kv_head), same(u.first), same(u.nq), same(u.begin), same(u.n);
+    return u;
+  }
+};
+
+// Walks a unit's query tiles: tile index and query head.
+struct QueryWalk {
+  int tile, head, first, last;
+  __device__ __forceinline__ QueryWalk(const DkvUnit& f, const AttnArgs& a)
+      : tile(f.first + f.begin % f.nq), head(f.kv_head * (a.heads / a.kv_heads) + f.begin / f.nq), first(f.first),
+        last(f.first + f.nq) {}
+  __device__ __forceinline__ void next() {
+    if (++tile == last) tile = first, ++head;
+  }
+};
+
 template <int DH>
 __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_constant__ CUtensorMap mq,
                                                                   const __grid_constant__ CUtensorMap mk,
@@ -939,7 +1065,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ __align__(8) uint64_t bars[11 + 2 * NS];
   __shared__ uint32_t tmem_at;
-  __shared__ volatile int32_t ids[4];
+  __shared__ DkvUnit given[4];
   __shared__ __align__(16) float row_lse[2][kTile], row_delta[2][kTile];
   const uint32_t k_at = bulk::smem_addr(smem), v_at = k_at + TB, qd_at = v_at + TB;
   const uint32_t bar = bulk::smem_addr(bars);
@@ -962,37 +1088,39 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
   tc::fence_after();
   wait_for_launch();
   const uint32_t s_at = tc::uni(tmem_at), dp_at = s_at + 128, dv_at = s_at + 256, dk_at = s_at + 256 + DH;
-  const int group = a.heads / a.kv_heads;
 
   if (warp == 9) {
     Feeder<DH, NS> feed(smem + 2 * TB, full, free, tail, a);
-    Taker take{int64_t(a.plan->ntiles) * a.kv_heads, &a.plan->next[1]};
+    Taker take{int64_t(a.plan->ntiles[1]) * a.kv_heads, &a.plan->next[1]};
     bool ok = true;
     int k = 0;
+    int32_t u = take.next();
     for (;; ++k) {
-      const int32_t u = take.next();
-      if (k > 0 && !(ok = feed.mend_all() && wait(kv_free, k - 1, a))) break;
-      if (lane == 0) ids[k & 3] = u;
-      if (u < 0) {
-        if (lane == 0) tc::arrive(kv_full);
-        break;
-      }
-      const Tile x = a.tiles[u / a.kv_heads];
-      const int kv_head = u % a.kv_heads;
-      int first;
-      const int nq = query_tiles(x, a.causal, first);
+      DkvUnit f;
+      f.n = -1;
+      if (u >= 0) f = DkvUnit(a.tiles[u / a.kv_heads], u % a.kv_heads, a).uniform();
+      if (lane == 0) given[k & 3] = f;
+      if (f.n < 0) break;
+      QueryWalk w(f, a);
+      auto put = [&]() {
+        const int at = w.tile * kTile;
+        const bool fine = feed.put(&mq, w.head, f.x.begin + at, f.x.L - at, true) &&
+                          feed.put(&mdo, w.head, f.x.begin + at, f.x.L - at, true);
+        w.next();
+        return fine;
+      };
+      if (!(ok = put())) break;
+      if (k > 0 && !(ok = wait(kv_free, k - 1, a))) break;
       if (lane == 0) {
         bulk::arrive_expect_tx(kv_full, 2 * TB);
-        load_tile<DH>(k_at, &mk, kv_head, x.begin + x.t * kTile, kv_full);
-        load_tile<DH>(v_at, &mv, kv_head, x.begin + x.t * kTile, kv_full);
+        load_tile<DH>(k_at, &mk, f.kv_head, f.x.begin + f.x.t * kTile, kv_full);
+        load_tile<DH>(v_at, &mv, f.kv_head, f.x.begin + f.x.t * kTile, kv_full);
       }
-      for (int h = kv_head * group; ok && h < (kv_head + 1) * group; ++h)
-        for (int j = 0; ok && j < nq; ++j) {
-          const int at = (first + j) * kTile;
-          ok = feed.put(&mq, h, x.begin + at, x.L - at, true) && feed.put(&mdo, h, x.begin + at, x.L - at, true);
-        }
-      if (!ok) break;
+      u = take.next();
+      for (int j = 1; ok && j < f.n; ++j) ok = put();
+      if (!ok || !(ok = feed.mend_all())) break;
     }
+    if (ok && (ok = k == 0 || wait(kv_free, k - 1, a)) && lane == 0) tc::arrive(kv_full);
     if (!ok) {
       bulk::warp_wait(kv_full, uint32_t(k) & 1u, a.wait_ns);
       feed.drain();
@@ -1004,41 +1132,41 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
     bool ok = true;
     // x^T overwrites p^T, v do^T overwrites ds^T: the products execute in the order they are issued
     auto scores = [&]() {
-      if (!wait(full + 8 * qs.s, qs.phase, a)) return false;
       mma_rows<DH>(s_at, k_at, qd_at + qs.s * TB);
       commit(s_full);
-      qs.skip2();
-      return true;
+      qs.skip(2);
     };
     auto products = [&]() {
-      if (!wait(full + 8 * ds.s, ds.phase, a)) return false;
       mma_rows<DH>(dp_at, v_at, qd_at + ds.s * TB);
       commit(dp_full);
-      ds.skip2();
-      return true;
+      ds.skip(2);
     };
     for (int k = 0; ok; ++k) {
       if (!(ok = wait(kv_full, k, a))) break;
-      const int32_t u = ids[k & 3];
-      if (u < 0) break;
-      const Tile x = a.tiles[u / a.kv_heads];
-      int first;
-      const int n = query_tiles(x, a.causal, first) * group;
-      if (!(ok = scores() && products())) break;
+      const int n = int(tc::uni(uint32_t(given[k & 3].n)));
+      if (n < 0) break;
+      if (!(ok = wait(full + 8 * qs.s, qs.phase, a))) break;
+      scores();
+      if (!(ok = wait(full + 8 * ds.s, ds.phase, a))) break;
+      products();
       if (n == 1) commit(kv_free);
       for (int j = 0; j < n; ++j, ++c) {
+        if (j + 1 < n && !(ok = wait(full + 8 * qs.s, qs.phase, a))) break;
         if (!(ok = wait(p_ready, c, a))) break;
         tc::fence_after();
         mma_cols<DH>(dv_at, s_at, s_at + 64, qd_at + dv.s * TB, j != 0);
         commit(free + 8 * dv.s);
-        dv.skip2();
-        if (j + 1 < n && !(ok = scores())) break;
+        dv.skip(2);
+        if (j + 1 < n) {
+          scores();
+          if (!(ok = wait(full + 8 * ds.s, ds.phase, a))) break;
+        }
         if (!(ok = wait(ds_ready, c, a))) break;
         tc::fence_after();
         mma_cols<DH>(dk_at, dp_at, dp_at + 64, qd_at + qk.s * TB, j != 0);
         commit(free + 8 * qk.s);
-        qk.skip2();
-        if (j + 1 < n && !(ok = products())) break;
+        qk.skip(2);
+        if (j + 1 < n) products();
         if (j + 2 == n) commit(kv_free);
       }
       if (ok) commit(sums_full);
@@ -1056,30 +1184,27 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!(ok = wait(kv_full, k, a))) break;
-      const int32_t u = ids[k & 3];
-      if (u < 0) break;
-      const Tile x = a.tiles[u / a.kv_heads];
-      const int kv_head = u % a.kv_heads;
-      int first;
-      const int nq = query_tiles(x, a.causal, first), n = nq * group;
+      const DkvUnit f = given[k & 3].uniform();
+      if (f.n < 0) break;
+      const Tile& x = f.x;
       const int key = x.t * kTile + r;
       // lse (in powers of two) or delta of query r of a tile; queries past the sample's end weigh nothing
-      auto row_value = [&](int tile, int head) {
-        const int i = tile * kTile + r;
-        const int64_t at = int64_t(head) * a.T + x.begin + i;
+      QueryWalk w(f, a);
+      auto row_value = [&]() {
+        const int i = w.tile * kTile + r;
+        const int64_t at = int64_t(w.head) * a.T + x.begin + i;
         if (half == 0) return i < x.L ? a.lse[at] * kLog2e : INFINITY;
         return i < x.L ? a.delta[at] : 0.f;
       };
-      int tile = first, head = kv_head * group;
-      float next = row_value(tile, head);
-      for (int j = 0; j < n; ++j, ++seen) {
+      float next = row_value();
+      for (int j = 0; j < f.n; ++j, ++seen) {
         // this tile's values are in for everyone (and everyone is done with the last tile but one's)
         (half == 0 ? row_lse : row_delta)[seen & 1][r] = next;
         __syncwarp();
         if (lane == 0) tc::arrive(rows_in);
-        const int i0 = tile * kTile;
-        if (++tile == first + nq) tile = first, ++head;
-        if (j + 1 < n) next = row_value(tile, head);
+        const int i0 = w.tile * kTile;
+        w.next();
+        if (j + 1 < f.n) next = row_value();
         if (!(ok = wait(rows_in, seen, a) && wait(s_full, seen, a))) break;
         tc::fence_after();
         float p[64];
@@ -1104,10 +1229,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
 #pragma unroll
           for (int i = 0; i < 64; ++i) p[i] = (i >= from || i == self) ? p[i] : 0.f;
         }
-        uint32_t w[32];
+        uint32_t pk[32];
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) w[i / 2] = tc::pack2(p[i], p[i + 1]);
-        tc::st32(s_at + lanes + cols, w);
+        for (int i = 0; i < 64; i += 2) pk[i / 2] = tc::pack2(p[i], p[i + 1]);
+        tc::st32(s_at + lanes + cols, pk);
         tc::wait_st();
         tc::fence_before();
         __syncwarp();
@@ -1128,11 +1253,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
             tc::add2(g + i + 2, -z.z, -z.w);
             tc::mul2(g + i, p[32 * b + i], p[32 * b + i + 1]);
             tc::mul2(g + i + 2, p[32 * b + i + 2], p[32 * b + i + 3]);
-            w[16 * b + i / 2] = tc::pack2(g[i], g[i + 1]);
-            w[16 * b + i / 2 + 1] = tc::pack2(g[i + 2], g[i + 3]);
+            pk[16 * b + i / 2] = tc::pack2(g[i], g[i + 1]);
+            pk[16 * b + i / 2 + 1] = tc::pack2(g[i + 2], g[i + 3]);
           }
         }
-        tc::st32(dp_at + lanes + cols, w);
+        tc::st32(dp_at + lanes + cols, pk);
         tc::wait_st();
         tc::fence_before();
         __syncwarp();
@@ -1140,17 +1265,53 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
       }
       if (!ok || !(ok = wait(sums_full, k, a))) break;
       tc::fence_after();
-      const int64_t pos = int64_t(x.begin) + key;
-      __nv_bfloat16* to = half == 0 ? a.dv + pos * a.dv_stride : a.dk + pos * a.dk_stride;
-      const uint32_t from = half == 0 ? dv_at : dk_at;
-      const float f = half == 0 ? 1.f : a.scale;
+      const int64_t pos = int64_t(x.begin) + key - lane;  // of the warp's first key
+      const int live = x.L - key + lane;
+      const int64_t stride = half == 0 ? a.dv_stride : a.dk_stride;
+      __nv_bfloat16* to = (half == 0 ? a.dv : a.dk) + pos * stride + f.kv_head * DH;
+      const uint32_t from = (half == 0 ? dv_at : dk_at) + lanes;
+      const float scale = half == 0 ? 1.f : a.scale;
+      const float4* other = nullptr;
+      if (x.split >= 0) {
+        const int64_t unit = int64_t(x.split) * a.kv_heads + f.kv_head;
+        float4* both = reinterpret_cast<float4*>(a.partial) + (unit * 8 + warp) * (2 * DH * 8);
+        float4* mine = both + x.part * (DH * 8);
+#pragma unroll
+        for (int b = 0; b < DH / 32; ++b) {
+          float g[32];
+          tc::ld32(from + 32 * b, g);
+          tc::wait_ld();
+          tc::tie32(g);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            __stcg(mine + (b * 8 + i) * 32 + lane, make_float4(g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]));
+        }
+        __threadfence();
+        __syncwarp();
+        int32_t first = 0;
+        if (lane == 0) first = atomicAdd(a.flags + unit * 8 + warp, 1);
+        first = __shfl_sync(0xffffffffu, first, 0);
+        if (first == 0) {
+          tc::fence_before();
+          continue;  // the other half adds them up
+        }
+        __threadfence();
+        other = both + (1 - x.part) * (DH * 8);
+      }
 #pragma unroll
       for (int b = 0; b < DH / 32; ++b) {
         float g[32];
-        tc::ld32(from + lanes + 32 * b, g);
+        tc::ld32(from + 32 * b, g);
         tc::wait_ld();
         tc::tie32(g);
-        if (key < x.L) store32(to + kv_head * DH + 32 * b, g, f);
+        if (other) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 z = __ldcg(other + (b * 8 + i) * 32 + lane);
+            g[4 * i] += z.x, g[4 * i + 1] += z.y, g[4 * i + 2] += z.z, g[4 * i + 3] += z.w;
+          }
+        }
+        store32(to + 32 * b, stride, live, g, scale);
       }
       tc::fence_before();
     }
@@ -1217,15 +1378,21 @@ int64_t most_tiles(int64_t T, int64_t S) { return T / kTile + (S < T ? S : T); }
 struct AttnWs {
   Plan* plan = nullptr;
   Tile *by_query = nullptr, *by_key = nullptr;
-  float* delta = nullptr;
+  float *delta = nullptr, *partial = nullptr;
+  int32_t* flags = nullptr;
 };
 
+// Both passes take the same workspace; the forward pass uses its first two parts.
 template <class Ws>
-void take_attn(int64_t T, int64_t S, int32_t Hq, Ws& ws, AttnWs& W) {
+void take_attn(int64_t T, int64_t S, int32_t Hq, int32_t Hkv, int32_t Dh, Ws& ws, AttnWs& W) {
+  const int64_t tiles = most_tiles(T, S), cut = most_split(sm_count());
+  const int64_t halves = tiles * Hkv < cut ? tiles * Hkv : cut;  // units cut in half
   W.plan = ws.template take<Plan>(1);
-  W.by_query = ws.template take<Tile>(size_t(most_tiles(T, S)));
-  W.by_key = ws.template take<Tile>(size_t(most_tiles(T, S)));
+  W.by_query = ws.template take<Tile>(size_t(tiles));
+  W.by_key = ws.template take<Tile>(size_t(2 * tiles < tiles + cut ? 2 * tiles : tiles + cut));
   W.delta = ws.template take<float>(size_t(Hq) * size_t(T));
+  W.flags = ws.template take<int32_t>(size_t(cut) * 8);
+  W.partial = ws.template take<float>(size_t(halves) * 2 * 2 * kTile * size_t(Dh));
 }
 
 // Allows a kernel its shared memory, once per device (`done` holds a bit for each).  A kernel
@@ -1273,7 +1440,7 @@ extern "C" size_t fs_jagged_attn_workspace_size(int64_t T, int64_t S, int32_t he
   if (T < 0 || S < 0 || heads < 1 || kv_heads < 1 || (head_dim != 64 && head_dim != 128)) return 0;
   WsCounter c;
   AttnWs W;
-  take_attn(T, S, heads, c, W);
+  take_attn(T, S, heads, kv_heads, head_dim, c, W);
   return c.used;
 }
 
@@ -1296,7 +1463,7 @@ extern "C" fs_status fs_jagged_attn(const void* q, int64_t q_stride, const void*
   if (most_tiles(T, S) * heads > INT32_MAX) return FS_ERR_INVALID_ARG;
   WsCursor cur(ws, ws_bytes);
   AttnWs W;
-  take_attn(T, S, heads, cur, W);
+  take_attn(T, S, heads, kv_heads, head_dim, cur, W);
   CUtensorMap mq, mk, mv;
   if (!encode(&mq, q, T, int64_t(heads) * head_dim, q_stride) || !encode(&mk, k, T, int64_t(kv_heads) * head_dim, k_stride) ||
       !encode(&mv, v, T, int64_t(kv_heads) * head_dim, v_stride))
@@ -1308,8 +1475,8 @@ extern "C" fs_status fs_jagged_attn(const void* q, int64_t q_stride, const void*
   a.wait_ns = uint64_t(spin_limit()) * 256u;
   const bool by_head = heads / kv_heads % 2 == 0;  // two heads of one tile share a block, else two tiles of one head
   const int parts = by_head ? heads / 2 : heads;
-  attn_plan_kernel<<<1, kPlanThreads, 0, st>>>(offsets, S, T, cand_len, a.causal, by_head ? 1 : 2, W.plan, W.by_query,
-                                               nullptr, err);
+  attn_plan_kernel<<<1, kPlanThreads, 0, st>>>(offsets, S, T, cand_len, a.causal, by_head ? 1 : 2, kv_heads, heads / kv_heads,
+                                               sm_count(), W.plan, W.by_query, nullptr, nullptr, err);
   const int64_t units = most_tiles(T, S) * parts;
   const int64_t grid = units < sm_count() ? units : sm_count();
   if (head_dim == 64) {
@@ -1347,33 +1514,33 @@ extern "C" fs_status fs_jagged_attn_backward(const void* q, int64_t q_stride, co
   if (most_tiles(T, S) * heads > INT32_MAX) return FS_ERR_INVALID_ARG;
   WsCursor cur(ws, ws_bytes);
   AttnWs W;
-  take_attn(T, S, heads, cur, W);
-  CUtensorMap mq, mk, mv, mdo;
+  take_attn(T, S, heads, kv_heads, head_dim, cur, W);
+  CUtensorMap mq, mk, mv, mo, mdo;
   if (!encode(&mq, q, T, ow, q_stride) || !encode(&mk, k, T, kw, k_stride) || !encode(&mv, v, T, kw, v_stride) ||
-      !encode(&mdo, dout, T, ow, ow))
+      !encode(&mo, out, T, ow, ow) || !encode(&mdo, dout, T, ow, ow))
     return FS_ERR_CUDA;
   AttnArgs a{};
   a.plan = W.plan;
   a.heads = heads, a.kv_heads = kv_heads, a.T = T, a.causal = causal != 0, a.scale = scale;
-  a.out = static_cast<const __nv_bfloat16*>(out), a.dout = static_cast<const __nv_bfloat16*>(dout);
-  a.lse = const_cast<float*>(lse), a.delta = W.delta, a.err = err;
+  a.lse = const_cast<float*>(lse), a.delta = W.delta, a.partial = W.partial, a.flags = W.flags, a.err = err;
   a.dq = static_cast<__nv_bfloat16*>(dq), a.dk = static_cast<__nv_bfloat16*>(dk), a.dv = static_cast<__nv_bfloat16*>(dv);
   a.dq_stride = dq_stride, a.dk_stride = dk_stride, a.dv_stride = dv_stride;
   a.wait_ns = uint64_t(spin_limit()) * 256u;
-  attn_plan_kernel<<<1, kPlanThreads, 0, st>>>(offsets, S, T, cand_len, a.causal, 1, W.plan, W.by_query, W.by_key, err);
+  attn_plan_kernel<<<1, kPlanThreads, 0, st>>>(offsets, S, T, cand_len, a.causal, 1, kv_heads, heads / kv_heads,
+                                               sm_count(), W.plan, W.by_query, W.by_key, W.flags, err);
   const int64_t tiles = most_tiles(T, S), sms = sm_count();
-  const int64_t gq = tiles * heads < sms ? tiles * heads : sms, gk = tiles * kv_heads < sms ? tiles * kv_heads : sms;
+  const int64_t gq = tiles * heads < sms ? tiles * heads : sms, gk = 2 * tiles * kv_heads < sms ? 2 * tiles * kv_heads : sms;
   AttnArgs b = a;
   a.tiles = W.by_query, b.tiles = W.by_key;
   if (head_dim == 64) {
     if (!prepare_kernel(attn_dq_kernel<64>, bwd_smem<64>(), 0, g_bwd_ready[0][0])) return FS_ERR_CUDA;
     if (!prepare_kernel(attn_dkv_kernel<64>, bwd_smem<64>(), 0, g_bwd_ready[0][1])) return FS_ERR_CUDA;
-    launch_after(attn_dq_kernel<64>, gq, kBwdThreads, bwd_smem<64>(), st, mq, mk, mv, mdo, a);
+    launch_after(attn_dq_kernel<64>, gq, kBwdThreads, bwd_smem<64>(), st, mq, mk, mv, mo, mdo, a);
     launch_after(attn_dkv_kernel<64>, gk, kBwdThreads, bwd_smem<64>(), st, mq, mk, mv, mdo, b);
   } else {
     if (!prepare_kernel(attn_dq_kernel<128>, bwd_smem<128>(), 0, g_bwd_ready[1][0])) return FS_ERR_CUDA;
     if (!prepare_kernel(attn_dkv_kernel<128>, bwd_smem<128>(), 0, g_bwd_ready[1][1])) return FS_ERR_CUDA;
-    launch_after(attn_dq_kernel<128>, gq, kBwdThreads, bwd_smem<128>(), st, mq, mk, mv, mdo, a);
+    launch_after(attn_dq_kernel<128>, gq, kBwdThreads, bwd_smem<128>(), st, mq, mk, mv, mo, mdo, a);
     launch_after(attn_dkv_kernel<128>, gk, kBwdThreads, bwd_smem<128>(), st, mq, mk, mv, mdo, b);
   }
   count_launch(3);
