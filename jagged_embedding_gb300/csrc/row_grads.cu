@@ -4,19 +4,22 @@
 // optimizer: what update_embedding receives, for callers that clip, average or
 // apply an optimizer of their own.
 //
-//   1. sort of (row, position): the library's radix passes, or one block in
-//      shared memory for a small batch (one launch instead of a dozen);
+//   1. sort of (row, position): the library's radix passes;
 //   2. heads: numbers the distinct rows of the sorted entries (single-pass scan);
 //   3. reduce: a group of lanes per tile of `chunk` sorted entries sums dout
 //      rows in fp32 in entry order; a row inside the tile is written out, a row
 //      that crosses a tile's edge leaves partial sums;
 //   4. join: adds the partial sums of the rows that cross edges, in tile order
 //      (a hot row crosses thousands of tiles: a whole block adds those).
+// A small batch (at most 8192 entries) takes two launches instead of sixteen: one block sorts and
+// numbers in shared memory, then a warp sums each distinct row.
 // The order of every sum follows from the sorted order and T alone: results are
 // the same bits from run to run.
 //
 // Bound by HBM: 8 B of ID and one row of dout per position, one row of G per
 // distinct ID; the sort moves about 20 B per ID and pass beside that.
+#include <atomic>
+
 #include "convert.cuh"
 #include "fs_common.cuh"
 #include "radix.cuh"
@@ -131,8 +134,8 @@ constexpr size_t small_smem() {
 
 template <int ITEMS>
 __global__ void __launch_bounds__(kSmallThreads, 1) small_sort_kernel(const int64_t* __restrict__ ids, int32_t T, int64_t R,
-                                                                      int kb, uint32_t* out_k, uint32_t* out_v,
-                                                                      int64_t* n_out, Numbering N, int32_t* err) {
+                                                                      int kb, uint32_t* out_v, Numbering N,
+                                                                      int32_t* err) {
   extern __shared__ uint32_t sm[];
   uint32_t* keys = sm;
   uint32_t* vals = keys + kSmallThreads * ITEMS;
@@ -225,20 +228,101 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_sort_kernel(const int6
   for (int i = 0; i < ITEMS; ++i) {
     const uint32_t p = threadIdx.x * ITEMS + i;
     if (p >= n) break;
-    if ((p & ((1u << N.chunk_log2) - 1u)) == 0) N.before[p >> N.chunk_log2] = u;
     if ((heads >> i) & 1u) {
       N.start[u] = p;
       if (int64_t(u) < N.cap) N.rows[u] = int64_t(keys[p]);
       else set_err(err, FS_ERR_CAPACITY);
       ++u;
     }
-    out_k[p] = keys[p];
     out_v[p] = vals[p];
   }
   if (threadIdx.x == 0) {
-    *n_out = n;
     *N.count = total;
     N.start[total] = n;
+  }
+}
+
+// Sums of a small batch: a warp per distinct row, LPR lanes (VEC columns each) a dout row, 32 / LPR
+// rows beside one another, kRedRows of them in flight per lane; their sums meet by
+// shuffles.  A row of more than kLongRow entries is taken by the block's eight warps.
+// blockIdx.y picks LPR * VEC columns of wider rows.
+constexpr int kSmallRowThreads = 256, kSmallRowWarps = kSmallRowThreads / 32, kLongRow = 256;
+
+template <class EI, class EO, int VEC, int LPR>
+__global__ void __launch_bounds__(kSmallRowThreads) grad_small_kernel(const uint32_t* __restrict__ vals,
+                                                                      const uint32_t* __restrict__ start,
+                                                                      const int64_t* __restrict__ count,
+                                                                      const void* __restrict__ dout, int32_t dim,
+                                                                      float scale, void* __restrict__ grads, int64_t cap) {
+  constexpr int SUB = 32 / LPR;
+  constexpr int SV = VEC * EO::kBytes > 16 ? VEC / 2 : VEC;  // columns of one store
+  __shared__ uint32_t long_row[kSmallRowWarps];
+  __shared__ float sums[kSmallRowWarps][LPR * VEC];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = lane / LPR, c = (int(blockIdx.y) * LPR + lane % LPR) * VEC;
+  const int64_t distinct = *count < cap ? *count : cap;
+  auto add = [&](float (&acc)[VEC], uint32_t e, uint32_t end, uint32_t step) {
+    for (; e < end; e += 8 * step) {
+      Raw<EI, VEC> g[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (e + q * step < end && c < dim) fetch<true>(g[q], dout, int64_t(__ldg(vals + e + q * step)) * dim + c);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (e + q * step < end && c < dim) {
+          float x[VEC];
+          unpack(g[q], x);
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) acc[k] += x[k];
+        }
+    }
+#pragma unroll
+    for (int o = LPR; o < 32; o <<= 1)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) acc[k] += __shfl_xor_sync(0xffffffffu, acc[k], o);
+  };
+  auto put = [&](int64_t u, float (&acc)[VEC]) {
+#pragma unroll
+    for (int k = 0; k < VEC; k += SV) {
+      float y[SV];
+#pragma unroll
+      for (int i = 0; i < SV; ++i) y[i] = acc[k + i] * scale;
+      store_vec<EO, SV, true>(grads, u * dim + c + k, y);
+    }
+  };
+  const int64_t u = int64_t(blockIdx.x) * kSmallRowWarps + warp;
+  bool is_long = false;
+  if (u < distinct) {
+    const uint32_t s = start[u], e = start[u + 1];
+    is_long = e - s > uint32_t(kLongRow);
+    if (!is_long) {
+      float acc[VEC];
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+      add(acc, s + sub, e, SUB);
+      if (sub == 0 && c < dim) put(u, acc);
+    }
+  }
+  if (lane == 0) long_row[warp] = is_long ? 1u : 0u;
+  __syncthreads();
+  for (int w = 0; w < kSmallRowWarps; ++w) {
+    if (!long_row[w]) continue;  // (the same for every thread)
+    const int64_t ul = int64_t(blockIdx.x) * kSmallRowWarps + w;
+    float acc[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+    add(acc, start[ul] + warp * SUB + sub, start[ul + 1], SUB * kSmallRowWarps);
+    if (sub == 0)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) sums[warp][(lane % LPR) * VEC + k] = acc[k];
+    __syncthreads();
+    if (warp == 0 && sub == 0 && c < dim) {
+      for (int q = 1; q < kSmallRowWarps; ++q)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) acc[k] += sums[q][(lane % LPR) * VEC + k];
+      put(ul, acc);
+    }
+    __syncthreads();
   }
 }
 
@@ -435,11 +519,11 @@ __global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const uint32_t*
 // ------------------------------------------------------------- host side
 
 // Entries per reduce tile: 8 for the smallest batches (one step of loads),
-// doubled while more than 32768 tiles remain, at most 128: enough groups of lanes to
+// doubled while more than 16384 tiles remain, at most 128: enough groups of lanes to
 // fill the GPU, few edges (each costs a partial row written and read).
 int chunk_log2_for(int64_t T) {
   int c = 3;
-  while (c < 7 && (T >> c) > 32768) ++c;
+  while (c < 7 && (T >> c) > 16384) ++c;
   return c;
 }
 
@@ -482,6 +566,37 @@ void launch_reduce_lpr(const GradLayout& L, const GradWs& G, const uint32_t* sk,
   grad_reduce_kernel<EI, EO, VEC, LPR><<<grid, kRedThreads, 0, st>>>(sk, sv, G.W.pass.n_valid, G.before, L.chunk_log2,
                                                                      dout, dim, scale, grads, cap, G.part_head,
                                                                      G.part_tail);
+}
+
+template <class EI, class EO, int VEC>
+void launch_small_vec(int64_t most_rows, const GradWs& G, const uint32_t* sv, const int64_t* count, const void* dout,
+                      int32_t dim, float scale, void* grads, int64_t cap, cudaStream_t st) {
+  const int chunks = (dim + VEC - 1) / VEC;
+  const int lpr = chunks <= 8 ? 8 : (chunks <= 16 ? 16 : 32);
+  const dim3 grid(unsigned((most_rows + kSmallRowWarps - 1) / kSmallRowWarps), unsigned((chunks + lpr - 1) / lpr));
+  auto go = [&](auto kern) { kern<<<grid, kSmallRowThreads, 0, st>>>(sv, G.start, count, dout, dim, scale, grads, cap); };
+  if (lpr == 8) go(grad_small_kernel<EI, EO, VEC, 8>);
+  else if (lpr == 16) go(grad_small_kernel<EI, EO, VEC, 16>);
+  else go(grad_small_kernel<EI, EO, VEC, 32>);
+}
+
+// The sort of a small batch: ITEMS entries a thread.  Its shared memory is allowed once per device.
+template <int ITEMS>
+bool launch_small_sort(const int64_t* ids, int64_t T, int64_t R, uint32_t* sv, const Numbering& N, int32_t* err,
+                       cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
+  if (!bit || !(ready.load(std::memory_order_relaxed) & bit)) {
+    if (cudaFuncSetAttribute(small_sort_kernel<ITEMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(small_smem<ITEMS>())) != cudaSuccess)
+      return false;
+    ready.fetch_or(bit);
+  }
+  const int kb = radix::bits_for(uint64_t(R));  // room for a key past every row
+  small_sort_kernel<ITEMS><<<1, kSmallThreads, small_smem<ITEMS>(), st>>>(ids, int32_t(T), R, kb, sv, N, err);
+  return true;
 }
 
 template <class EI, class EO, int VEC>
@@ -534,16 +649,16 @@ extern "C" fs_status fs_emb_grad_rows(int64_t num_rows, int32_t dim, const int64
   const Numbering N{rows, cap_rows, count, G.start, G.before, L.chunk_log2};
   int launches = 0;
   uint32_t *sk = G.W.k[0], *sv = G.W.v[0];
-  if (T <= kSmallMax) {
-    const int kb = radix::bits_for(uint64_t(num_rows));  // room for a key past every row
-    auto small = [&](auto kern, size_t smem) {
-      radix::set_smem(kern, smem);
-      kern<<<1, kSmallThreads, smem, st>>>(ids, int32_t(T), num_rows, kb, sk, sv, G.W.pass.n_valid, N, err);
-    };
-    if (T <= kSmallThreads) small(small_sort_kernel<1>, small_smem<1>());
-    else if (T <= kSmallThreads * 2) small(small_sort_kernel<2>, small_smem<2>());
-    else if (T <= kSmallThreads * 4) small(small_sort_kernel<4>, small_smem<4>());
-    else small(small_sort_kernel<8>, small_smem<8>());
+  const bool small = T <= kSmallMax;
+  if (small) {
+    bool ok;
+    if (T <= kSmallThreads) ok = launch_small_sort<1>(ids, T, num_rows, sv, N, err, st);
+    else if (T <= kSmallThreads * 2) ok = launch_small_sort<2>(ids, T, num_rows, sv, N, err, st);
+    else if (T <= kSmallThreads * 3) ok = launch_small_sort<3>(ids, T, num_rows, sv, N, err, st);
+    else if (T <= kSmallThreads * 4) ok = launch_small_sort<4>(ids, T, num_rows, sv, N, err, st);
+    else if (T <= kSmallThreads * 6) ok = launch_small_sort<6>(ids, T, num_rows, sv, N, err, st);
+    else ok = launch_small_sort<8>(ids, T, num_rows, sv, N, err, st);
+    if (!ok) return FS_ERR_CUDA;
     launches += 1;
   } else {
     const fs_status s = radix::run_sort(SrcIds{ids, num_rows}, L.plan, G.W, err, st, &sk, &sv, &launches);
@@ -557,16 +672,23 @@ extern "C" fs_status fs_emb_grad_rows(int64_t num_rows, int32_t dim, const int64
   const int vec = ib == 4 ? 4 : 8;
   // 16-byte loads of dout where rows and addresses allow them, element by element otherwise
   const bool wide = dim % vec == 0 && aligned(dout, 16) && aligned(row_grads, 16);
-#define FS_GRAD(EI, EO, V)                                                                          \
-  do {                                                                                              \
-    if (wide) launch_reduce_vec<EI, EO, V>(L, G, sk, sv, dout, dim, scale, row_grads, cap_rows, st); \
-    else launch_reduce_vec<EI, EO, 1>(L, G, sk, sv, dout, dim, scale, row_grads, cap_rows, st);      \
+  const int64_t most_rows = T < num_rows ? T : num_rows;
+#define FS_GRAD(EI, EO, V)                                                                                        \
+  do {                                                                                                            \
+    if (small && wide) launch_small_vec<EI, EO, V>(most_rows, G, sv, count, dout, dim, scale, row_grads, cap_rows, st); \
+    else if (small) launch_small_vec<EI, EO, 1>(most_rows, G, sv, count, dout, dim, scale, row_grads, cap_rows, st);    \
+    else if (wide) launch_reduce_vec<EI, EO, V>(L, G, sk, sv, dout, dim, scale, row_grads, cap_rows, st);         \
+    else launch_reduce_vec<EI, EO, 1>(L, G, sk, sv, dout, dim, scale, row_grads, cap_rows, st);                   \
   } while (0)
   if (ib == 4 && ob == 4) FS_GRAD(F32, F32, 4);
   else if (ib == 4) FS_GRAD(F32, Bf16, 4);
   else if (ob == 4) FS_GRAD(Bf16, F32, 8);
   else FS_GRAD(Bf16, Bf16, 8);
 #undef FS_GRAD
+  if (small) {
+    count_launch(launches + 1);
+    return launch_status();
+  }
   const int64_t want = (L.tiles + kJoinWarps - 1) / kJoinWarps, most = int64_t(sm_count()) * 8;
   auto join = [&](auto kern) {
     kern<<<unsigned(want < most ? want : most), kJoinThreads, 0, st>>>(sk, G.W.pass.n_valid, G.start, G.before,
