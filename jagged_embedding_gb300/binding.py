@@ -602,7 +602,7 @@ def fs_emb_update_sorted(table, state, grads, T, ws, optim, lr, eps=0.0, phase=P
 
 def _same(t, shape, dtype, name, device):
     """An output or second operand: exactly this shape and type, contiguous, on the same device."""
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise FsError(1, f"{name} must be a contiguous {shape} tensor of {dtype} on {device}")
 
 

@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kSmallRowThreads) grad_small_kernel(const uint
 
 // ------------------------------------------------------------- reduce
 
-constexpr int kRedThreads = 256, kRedRows = 8;  // dout rows in flight per lane
+constexpr int kRedThreads = 128, kRedRows = 8;  // dout rows in flight per lane
 
 // LPR lanes (VEC columns each) per tile of 2^chunk_log2 sorted entries;
 // blockIdx.y picks LPR * VEC columns of wider rows.  kRedRows dout rows are in
@@ -336,7 +336,7 @@ constexpr int kRedThreads = 256, kRedRows = 8;  // dout rows in flight per lane
 // loaded before this step's rows.  (The key and position arrays are padded to
 // 64 entries, so a step's vector loads stay inside them.)
 template <class EI, class EO, int VEC, int LPR>
-__global__ void __launch_bounds__(kRedThreads, 3) grad_reduce_kernel(
+__global__ void __launch_bounds__(kRedThreads, 6) grad_reduce_kernel(
     const uint32_t* __restrict__ keys, const uint32_t* __restrict__ vals, const int64_t* __restrict__ n_dev,
     const uint32_t* __restrict__ before, int chunk_log2, const void* __restrict__ dout, int32_t dim, float scale,
     void* __restrict__ grads, int64_t cap, float* __restrict__ part_head, float* __restrict__ part_tail) {
@@ -422,9 +422,9 @@ __global__ void __launch_bounds__(kRedThreads, 3) grad_reduce_kernel(
 // One warp per tile in which a row begins that goes on in the next tile:
 // the row's sum is the tile's tail plus the heads of the following tiles up to
 // the row's last.  Rows over more than kLongTiles tiles are added by the whole
-// block: warp w takes every 8th tile, then the warps' sums in warp order.
+// block: warp w takes every 32nd tile, then the warps' sums in warp order.
 // VEC columns a lane.
-constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kLongTiles = 16;
+constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32, kLongTiles = 16;
 
 template <class EO, int VEC>
 __global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const uint32_t* __restrict__ keys,
@@ -519,11 +519,12 @@ __global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const uint32_t*
 // ------------------------------------------------------------- host side
 
 // Entries per reduce tile: 8 for the smallest batches (one step of loads),
-// doubled while more than 16384 tiles remain, at most 128: enough groups of lanes to
+// doubled while more than 8192 tiles remain, at most 64 (2M entries of 128 bf16: 306 us a pass with 64 and with 128
+// 316, 32 324): enough groups of lanes to
 // fill the GPU, few edges (each costs a partial row written and read).
 int chunk_log2_for(int64_t T) {
   int c = 3;
-  while (c < 7 && (T >> c) > 16384) ++c;
+  while (c < 6 && (T >> c) > 8192) ++c;
   return c;
 }
 
