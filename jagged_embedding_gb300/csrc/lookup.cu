@@ -19,7 +19,7 @@ constexpr int kLookupThreads = 256;
 // Bound by HBM: 8 B of ID, one table row (distinct rows once, the others from
 // L2) and one output row per position.
 template <class EI, class EO, int VEC, int LPR>
-__global__ void __launch_bounds__(kLookupThreads, 4) lookup_kernel(const void* __restrict__ table, int64_t R, int32_t dim,
+__global__ void __launch_bounds__(kLookupThreads, 3) lookup_kernel(const void* __restrict__ table, int64_t R, int32_t dim,
                                                                    const int64_t* __restrict__ ids, int64_t T,
                                                                    float scale, void* __restrict__ out, int32_t* err) {
   constexpr int RPI = 32 / LPR;

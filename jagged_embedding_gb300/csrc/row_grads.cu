@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_sort_kernel(const int6
                                                                       int kb, uint32_t* out_v, Numbering N,
                                                                       int32_t* err) {
   extern __shared__ uint32_t sm[];
+  asm volatile("griddepcontrol.launch_dependents;");
   uint32_t* keys = sm;
   uint32_t* vals = keys + kSmallThreads * ITEMS;
   uint32_t* hist = vals + kSmallThreads * ITEMS;  // [warps][digits]
@@ -182,14 +183,19 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_sort_kernel(const int6
       __syncwarp();
     }
     __syncthreads();
-    // thread d: digit d's entries, exclusive over the warps, then over the digits
+    // thread d: digit d's entries, exclusive over the warps (all read before any is
+    // written: one latency instead of 32), then over the digits
     uint32_t tot = 0;
-    if (int(threadIdx.x) < nb)
+    if (int(threadIdx.x) < nb) {
+      uint32_t c[kSmallWarps];
+#pragma unroll
+      for (int w = 0; w < kSmallWarps; ++w) c[w] = hist[w * nb + threadIdx.x];
+#pragma unroll
       for (int w = 0; w < kSmallWarps; ++w) {
-        const uint32_t c = hist[w * nb + threadIdx.x];
         hist[w * nb + threadIdx.x] = tot;
-        tot += c;
+        tot += c[w];
       }
+    }
     uint32_t all;
     const uint32_t first = block_exclusive_scan<uint32_t>(tot, red, &all);
     if (int(threadIdx.x) < nb) dstart[threadIdx.x] = first;
@@ -246,7 +252,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_sort_kernel(const int6
 // rows beside one another, kRedRows of them in flight per lane; their sums meet by
 // shuffles.  A row of more than kLongRow entries is taken by the block's eight warps.
 // blockIdx.y picks LPR * VEC columns of wider rows.
-constexpr int kSmallRowThreads = 256, kSmallRowWarps = kSmallRowThreads / 32, kLongRow = 256;
+constexpr int kSmallRowThreads = 256, kSmallRowWarps = kSmallRowThreads / 32, kLongRow = 48;
 
 template <class EI, class EO, int VEC, int LPR>
 __global__ void __launch_bounds__(kSmallRowThreads) grad_small_kernel(const uint32_t* __restrict__ vals,
@@ -260,6 +266,7 @@ __global__ void __launch_bounds__(kSmallRowThreads) grad_small_kernel(const uint
   __shared__ float sums[kSmallRowWarps][LPR * VEC];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / LPR, c = (int(blockIdx.y) * LPR + lane % LPR) * VEC;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (launched while the sort still runs)
   const int64_t distinct = *count < cap ? *count : cap;
   auto add = [&](float (&acc)[VEC], uint32_t e, uint32_t end, uint32_t step) {
     for (; e < end; e += 8 * step) {
@@ -575,7 +582,18 @@ void launch_small_vec(int64_t most_rows, const GradWs& G, const uint32_t* sv, co
   const int chunks = (dim + VEC - 1) / VEC;
   const int lpr = chunks <= 8 ? 8 : (chunks <= 16 ? 16 : 32);
   const dim3 grid(unsigned((most_rows + kSmallRowWarps - 1) / kSmallRowWarps), unsigned((chunks + lpr - 1) / lpr));
-  auto go = [&](auto kern) { kern<<<grid, kSmallRowThreads, 0, st>>>(sv, G.start, count, dout, dim, scale, grads, cap); };
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kSmallRowThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto go = [&](auto kern) {
+    cudaLaunchKernelEx(&cfg, kern, sv, static_cast<const uint32_t*>(G.start), count, dout, dim, scale, grads, cap);
+  };
   if (lpr == 8) go(grad_small_kernel<EI, EO, VEC, 8>);
   else if (lpr == 16) go(grad_small_kernel<EI, EO, VEC, 16>);
   else go(grad_small_kernel<EI, EO, VEC, 32>);
