@@ -820,7 +820,10 @@ __device__ __forceinline__ Tile uniform_tile(Tile x) {
 // the 128 keys.  Per key tile: x = q k^T and do v^T into 128 columns each; p = exp(x - lse)
 // stays in registers and frees x, so the next tile's x is computed while
 // ds = p * (do v^T - delta) is formed; ds (bf16) goes over do v^T and multiplies k.
-// The unit's rows of out come through the ring in front of its keys, for delta.
+// delta = dout.out: the unit's rows of out come through the ring in front of its
+// keys.  Where there is one key tile delta = sum p * (do v^T) is at hand instead, free of the rounding
+// of out, which matters most there: few keys leave out about as large as v (8 samples of up to
+// 511 positions: dq and dk 2.6e-3 from 64 bits with dout.out, 2.4e-3 with the sum; bf16 results alone are 1.7e-3).
 struct DqUnit {
   Tile x;
   int head, kv_head, nk, n;  // n < 0: no more units
@@ -894,7 +897,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                feed.put(&mv, f.kv_head, f.x.begin + at, f.x.L - at, false);
       };
       const int at = f.x.begin + f.x.t * kTile;
-      if (!(ok = feed.put(&mo, f.head, at, kTile, false) && put(0))) break;
+      if (!(ok = (f.n == 1 || feed.put(&mo, f.head, at, kTile, false)) && put(0))) break;
       if (k > 0 && !(ok = wait(q_free, k - 1, a))) break;
       if (lane == 0) {
         bulk::arrive_expect_tx(q_full, 2 * TB);
@@ -932,7 +935,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
       if (!(ok = wait(q_full, k, a))) break;
       const int n = int(tc::uni(uint32_t(given[k & 3].n)));
       if (n < 0) break;
-      ks.skip(1), vs.skip(1), kq.skip(1);  // (the tile of out)
+      if (n > 1) ks.skip(1), vs.skip(1), kq.skip(1);  // (the tile of out)
       if (!(ok = scores() && wait(full + 8 * vs.s, vs.phase, a))) break;
       products();
       for (int j = 0; j < n; ++j) {
@@ -971,36 +974,46 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
       const bool live = row < x.L;
       const int64_t pos = int64_t(x.begin) + row;
       const float lse2 = live ? a.lse[int64_t(f.head) * a.T + pos] * kLog2e : 0.f;
-      // delta = dout.out of the row, half of the columns each, from the loaded tiles (16-byte pieces of
-      // a row lie swizzled: piece c of row r at c ^ (r & 7))
-      const int o_slot = int(item % NS);
-      if (!(ok = wait(full + 8 * o_slot, item / NS, a))) break;
-      item += 1 + 2 * uint32_t(f.n);
-      float d = 0.f;
+      // half of the row's sum each; then everyone's is in
+      auto join_delta = [&](float d, float& delta) {
+        half_delta[half][r] = d;
+        __syncwarp();
+        if (lane == 0) tc::arrive(delta_in);
+        if (!wait(delta_in, k, a)) return false;
+        delta = half_delta[0][r] + half_delta[1][r];
+        if (live && half == 0) a.delta[int64_t(f.head) * a.T + pos] = delta;
+        return true;
+      };
+      float delta = 0.f;
+      if (f.n > 1) {
+        // from the loaded tiles (16-byte pieces of a row lie swizzled: piece c of row r at c ^ (r & 7))
+        const int o_slot = int(item % NS);
+        if (!(ok = wait(full + 8 * o_slot, item / NS, a))) break;
+        float d = 0.f;
 #pragma unroll
-      for (int i = 0; i < DH / 16; ++i) {
-        const int piece = half * (DH / 16) + i;
-        const int at = (piece / 8) * kBox + r * 128 + (((piece % 8) ^ (r & 7)) * 16);
-        const uint4 v = *reinterpret_cast<const uint4*>(smem + (2 + o_slot) * TB + at);
-        const uint4 w = *reinterpret_cast<const uint4*>(smem + TB + at);
-        const uint32_t vv[4] = {v.x, v.y, v.z, v.w}, ww[4] = {w.x, w.y, w.z, w.w};
+        for (int i = 0; i < DH / 16; ++i) {
+          const int piece = half * (DH / 16) + i;
+          const int at = (piece / 8) * kBox + r * 128 + (((piece % 8) ^ (r & 7)) * 16);
+          const uint4 v = *reinterpret_cast<const uint4*>(smem + (2 + o_slot) * TB + at);
+          const uint4 w = *reinterpret_cast<const uint4*>(smem + TB + at);
+          const uint32_t vv[4] = {v.x, v.y, v.z, v.w}, ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          d = fmaf(__uint_as_float(vv[q] << 16), __uint_as_float(ww[q] << 16), d);
-          d = fmaf(__uint_as_float(vv[q] & 0xFFFF0000u), __uint_as_float(ww[q] & 0xFFFF0000u), d);
+          for (int q = 0; q < 4; ++q) {
+            d = fmaf(__uint_as_float(vv[q] << 16), __uint_as_float(ww[q] << 16), d);
+            d = fmaf(__uint_as_float(vv[q] & 0xFFFF0000u), __uint_as_float(ww[q] & 0xFFFF0000u), d);
+          }
         }
+        if (!(ok = join_delta(d, delta))) break;
+        if (threadIdx.x == 0) {  // everyone has read the tiles of out and dout
+          tc::arrive(free + 8 * o_slot);
+          tc::arrive(q_free);
+        }
+        __syncwarp();
+      } else {
+        if (threadIdx.x == 0) tc::arrive(q_free);
+        __syncwarp();
       }
-      half_delta[half][r] = d;
-      __syncwarp();
-      if (lane == 0) tc::arrive(delta_in);
-      if (!(ok = wait(delta_in, k, a))) break;
-      if (threadIdx.x == 0) {  // everyone has read the tiles of out and dout
-        tc::arrive(free + 8 * o_slot);
-        tc::arrive(q_free);
-      }
-      __syncwarp();
-      const float delta = half_delta[0][r] + half_delta[1][r];
-      if (live && half == 0) a.delta[int64_t(f.head) * a.T + pos] = delta;
+      item += (f.n > 1 ? 1u : 0u) + 2 * uint32_t(f.n);
       for (int j = 0; j < f.n; ++j, ++seen) {
         if (!(ok = wait(s_full, seen, a))) break;
         tc::fence_after();
@@ -1024,6 +1037,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
         }
         if (!(ok = wait(dp_full, seen, a))) break;
         tc::fence_after();
+        if (f.n == 1) {
+          float d = 0.f;
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            float g[32];
+            tc::ld32(dp_at + lanes + cols + 32 * b, g);
+            tc::wait_ld();
+            tc::tie32(g);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!masked || 32 * b + i < lim || 32 * b + i == self) d = fmaf(p[32 * b + i], g[i], d);
+          }
+          if (!(ok = join_delta(d, delta))) break;
+        }
         uint32_t w[32];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
