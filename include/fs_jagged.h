@@ -566,7 +566,8 @@ fs_status fs_jagged_attn_backward(const void* q, int64_t q_stride, const void* k
  *   tests and benchmarks, not for the hot loop.
  * fs_set_spin_limit: polls before a bounded inter-block wait gives up with
  *   FS_ERR_TIMEOUT (default 1<<22, roughly a second); a wait for a bulk copy
- *   of gradient rows gives up after polls * 256 ns.  Applies to later calls.
+ *   of gradient rows, and every wait inside the attention kernels, gives up after
+ *   polls * 256 ns.  Applies to later calls.
  *   The Python binding applies the environment variable FS_SPIN_LIMIT (a
  *   positive integer) when it loads the library.
  * fs_get_spin_limit: the limit in force.
@@ -576,8 +577,9 @@ fs_status fs_jagged_attn_backward(const void* q, int64_t q_stride, const void* k
  *   skips publishing its look-back status, so every later tile's wait runs out
  *   and the call reports FS_ERR_TIMEOUT instead of hanging; in the embedding
  *   update, the first bulk copy of gradient rows for sorted tile `tile` is
- *   never issued, so the wait for it runs out the same way.  -1 (the default)
- *   turns it off.  Never used outside tests.
+ *   never issued, so the wait for it runs out the same way; in the attention
+ *   kernels, the first tile that block `tile` loads after its queries (keys) is
+ *   never loaded.  -1 (the default) turns it off.  Never used outside tests.
  * ---------------------------------------------------------------------- */
 fs_status fs_check(const int32_t* err, fs_stream_t stream);
 const char* fs_status_string(fs_status s);

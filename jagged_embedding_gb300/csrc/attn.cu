@@ -240,6 +240,7 @@ struct AttnArgs {
   int64_t dq_stride, dk_stride, dv_stride;
   int32_t* err;
   uint64_t wait_ns;
+  int64_t skip_block;  // test hook: the first tile of this block's ring is never loaded (-1: none)
 };
 
 // Wait of a whole warp for a barrier's phase, with a limit.  The hand-overs
@@ -324,6 +325,10 @@ struct Feeder {
       if (mended != tails && !__all_sync(0xffffffffu, bulk::try_wait(free + 8 * s, phase & 1u)) && !mend_all())
         return false;
       if (!wait(free + 8 * s, phase, a)) return false;
+    }
+    if (slot == 0 && a.skip_block == int64_t(blockIdx.x)) {
+      ++slot;
+      return true;
     }
     uint32_t bar = full + 8 * s;
     if (mend_tail && valid < kTile) {
@@ -677,7 +682,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
           if (j > 0) commit(free + 8 * v.s);
           if (j < f.n) commit(free + 8 * key.s);
           if (j == f.n - 1) commit(q_free);
-          if (j == f.n) commit(o_full);
+          if (j == f.n) {  // (a barrier for each: a warpgroup without work would fall phases behind one of both)
+            commit(o_full);
+            if (f.both) commit(o_full + 8);
+          }
         }
         ks.back(2);  // (the last step has no key tile)
       }
@@ -693,7 +701,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t x_at = s_at + 128 * i + lanes, acc_at = o_at + DH * i + lanes;
     const float c = a.scale * kLog2e;
-    uint32_t seen = 0;
+    uint32_t seen = 0, units = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!(ok = wait(q_full, k, a))) break;
@@ -701,10 +709,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
       if (f.n < 0) break;
       __syncwarp();
       if (lane == 0) tc::arrive(q_free);  // (a warpgroup without work in this unit keeps step with the others)
-      if (i == 1 && !f.both) {
-        if (!(ok = wait(o_full, k, a))) break;
-        continue;
-      }
+      if (i == 1 && !f.both) continue;
       const int tile = i ? f.row1 : f.row0;
       const int row = tile * kTile + int(threadIdx.x & 127);  // position inside the sample
       float m = -INFINITY, l = 0.f;
@@ -780,7 +785,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
         __syncwarp();
         if (lane == 0) tc::arrive(p_ready + 8 * i);
       }
-      if (!ok || !(ok = wait(o_full, k, a))) break;
+      if (!ok || !(ok = wait(o_full + 8 * i, units, a))) break;
+      ++units;
       tc::fence_after();
       const int64_t pos = int64_t(f.x.begin) + row;
       const int head = i ? f.head1 : f.head0;
@@ -864,7 +870,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
   const int warp = int(tc::uni(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (warp == 8) {
     if (lane == 0) {
-      for (int i = 0; i < 11 + 2 * NS; ++i) bulk::mbar_init(bar + 8 * i, i == 1 ? 2 : (i >= 4 && i <= 6 ? 8 : 1));
+      for (int i = 0; i < 11 + 2 * NS; ++i) bulk::mbar_init(bar + 8 * i, i == 1 ? 9 : (i >= 4 && i <= 6 ? 8 : 1));
       bulk::fence_init();
     }
     __syncwarp();
@@ -1004,15 +1010,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
           }
         }
         if (!(ok = join_delta(d, delta))) break;
-        if (threadIdx.x == 0) {  // everyone has read the tiles of out and dout
-          tc::arrive(free + 8 * o_slot);
-          tc::arrive(q_free);
-        }
-        __syncwarp();
-      } else {
-        if (threadIdx.x == 0) tc::arrive(q_free);
+        if (threadIdx.x == 0) tc::arrive(free + 8 * o_slot);  // everyone has read the tiles of out and dout
         __syncwarp();
       }
+      if (lane == 0) tc::arrive(q_free);  // (every warp has its say: none falls phases behind q_full)
+      __syncwarp();
       item += (f.n > 1 ? 1u : 0u) + 2 * uint32_t(f.n);
       for (int j = 0; j < f.n; ++j, ++seen) {
         if (!(ok = wait(s_full, seen, a))) break;
@@ -1153,7 +1155,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
   const int warp = int(tc::uni(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (warp == 8) {
     if (lane == 0) {
-      for (int i = 0; i < 11 + 2 * NS; ++i) bulk::mbar_init(bar + 8 * i, i >= 4 && i <= 6 ? 8 : 1);
+      for (int i = 0; i < 11 + 2 * NS; ++i) bulk::mbar_init(bar + 8 * i, i == 1 ? 9 : (i >= 4 && i <= 6 ? 8 : 1));
       bulk::fence_init();
     }
     __syncwarp();
@@ -1264,6 +1266,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
       if (!(ok = wait(kv_full, k, a))) break;
       const DkvUnit f = given[k & 3].uniform();
       if (f.n < 0) break;
+      __syncwarp();
+      if (lane == 0) tc::arrive(kv_free);  // (every warp has its say: none falls phases behind kv_full)
       const Tile& x = f.x;
       const int key = x.t * kTile + r;
       // lse (in powers of two) or delta of query r of a tile; queries past the sample's end weigh nothing
@@ -1556,7 +1560,7 @@ extern "C" fs_status fs_jagged_attn(const void* q, int64_t q_stride, const void*
   a.heads = heads, a.kv_heads = kv_heads, a.T = T, a.causal = causal != 0, a.scale = scale;
   a.offsets = offsets, a.cand = cand_len, a.S = int32_t(S);
   a.o = static_cast<__nv_bfloat16*>(out), a.lse = lse, a.err = err;
-  a.wait_ns = uint64_t(spin_limit()) * 256u;
+  a.wait_ns = uint64_t(spin_limit()) * 256u, a.skip_block = debug_skip_tile();
   const bool by_head = heads / kv_heads % 2 == 0;  // two heads of one tile share a block, else two tiles of one head
   const int parts = by_head ? heads / 2 : heads;
   const int64_t units = most_tiles(T, S) * parts;
@@ -1614,7 +1618,7 @@ extern "C" fs_status fs_jagged_attn_backward(const void* q, int64_t q_stride, co
   a.lse = const_cast<float*>(lse), a.delta = W.delta, a.partial = W.partial, a.flags = W.flags, a.err = err;
   a.dq = static_cast<__nv_bfloat16*>(dq), a.dk = static_cast<__nv_bfloat16*>(dk), a.dv = static_cast<__nv_bfloat16*>(dv);
   a.dq_stride = dq_stride, a.dk_stride = dk_stride, a.dv_stride = dv_stride;
-  a.wait_ns = uint64_t(spin_limit()) * 256u;
+  a.wait_ns = uint64_t(spin_limit()) * 256u, a.skip_block = debug_skip_tile();
   const bool listed = !each_its_own(S, most_tiles(T, S) * heads);
   if (listed)
     attn_plan_kernel<<<1, kPlanThreads, 0, st>>>(offsets, S, T, cand_len, a.causal, 1, kv_heads, heads / kv_heads,

@@ -297,3 +297,63 @@ def test_nothing_to_do():
     B.check(err)
     dq, dk, dv, err = B.fs_jagged_attn_backward(x, x, x, out, lse, x, torch.zeros(3, dtype=torch.int64, device=DEV), 0.1)
     B.check(err)
+
+
+def test_many_units_a_block_and_heavy_key_tiles_in_halves():
+    """More units than SMs (lists, several units a block), and a batch in which a few long samples hold most of the
+    work, so that their key tiles are cut in half."""
+    lens = [(37 * i) % 331 for i in range(60)]
+    _check(Case(lens, 4, 2, 64, cand=[min(n, i % 5) for i, n in enumerate(lens)]))
+    _check(Case(lens, 3, 3, 128, causal=False))
+    heavy = [1700, 1500] + [20 + i for i in range(40)]
+    a = _check(Case(heavy, 8, 2, 128))
+    b = _check(Case(heavy, 8, 2, 128))
+    assert torch.equal(a[2], b[2])  # (which half comes first does not show)
+    _check(Case(heavy, 4, 1, 64, causal=False, cand=[min(n, 64) for n in heavy]))
+
+
+@pytest.mark.parametrize("S", [32, 33])
+def test_around_the_batch_without_lists(S):
+    lens = [3 + 2 * i for i in range(S)]
+    _check(Case(lens, 2, 2, 64, cand=[i % 3 for i in range(S)]))
+
+
+def test_empty_samples_only():
+    c = Case([0] * 40, 2, 1, 64, tail=50)
+    out, lse, err = c.forward()
+    B.check(err)
+    c.backward(out, lse, err=err)
+    B.check(err)
+
+
+@pytest.mark.parametrize("Dh", [64, 128])
+@pytest.mark.parametrize("lens", [[400], [90, 700, 5], [50] * 40])
+def test_waits_that_run_out(Dh, lens):
+    """A tile that is never loaded: every wait ends, the error word says so, and the context stays usable."""
+    c = Case(lens, 2, 2, Dh)
+    want = c.forward()
+    B.check(want[2])
+    grads = c.backward(want[0], want[1])
+    B.check(grads[3])
+    before = B.spin_limit()
+    try:
+        B.set_spin_limit(2000)  # about half a millisecond a wait
+        B.debug_skip_publish(0)
+        _, _, err = c.forward()
+        with pytest.raises(B.FsError) as e:
+            B.check(err)
+        assert e.value.code == 6
+        _, _, _, err = c.backward(want[0], want[1])
+        with pytest.raises(B.FsError) as e:
+            B.check(err)
+        assert e.value.code == 6
+    finally:
+        B.debug_skip_publish(-1)
+        B.set_spin_limit(before)
+    again = c.forward()
+    B.check(again[2])
+    m = c.inside()
+    assert torch.equal(again[0][m], want[0][m])
+    g2 = c.backward(want[0], want[1])
+    B.check(g2[3])
+    assert all(torch.equal(x[m], y[m]) for x, y in zip(grads[:3], g2[:3]))
