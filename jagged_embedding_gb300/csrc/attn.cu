@@ -285,34 +285,54 @@ __device__ __forceinline__ void zero_rows(unsigned char* tile, int from) {
 
 // The loading warp's side of a ring of NS tile slots in shared memory, filled in
 // order.  full[s]: the tile has arrived; free[s]: its last reader is done.  A
-// tile with rows past its sample's end arrives on a barrier of its own
-// (tail[2]), is mended here, and only then reported full; the mending waits until the ring
-// would block anyway, at most two tiles outstanding.
+// tile with rows past its sample's end (a tail) arrives on a barrier of its own
+// (tail[4]), is mended here, and only then reported full.  Whenever this warp has to wait for something
+// it mends what has arrived in the meantime, so that neither holds up the other.
 template <int DH, int NS>
 struct Feeder {
   static constexpr int TB = DH / 64 * kBox;
   unsigned char* tiles;
   uint32_t full, free, tail;
   const AttnArgs& a;
-  uint32_t slot = 0;             // tiles asked for
-  uint32_t tails = 0, mended = 0;
-  int tail_slot[2] = {0, 0}, tail_rows[2] = {0, 0};
+  uint32_t slot = 0;              // tiles asked for
+  uint32_t tails = 0, mended = 0; // at most four outstanding
+  uint64_t notes = 0;             // of those, the oldest in the low bits: slot | first foreign row << 8, 16 bits each
 
   __device__ __forceinline__ Feeder(unsigned char* tiles, uint32_t full, uint32_t free, uint32_t tail, const AttnArgs& a)
       : tiles(tiles), full(full), free(free), tail(tail), a(a) {}
 
-  __device__ __forceinline__ bool mend() {  // the oldest tail
-    const uint32_t w = mended & 1u;
-    if (!wait(tail + 8 * w, mended >> 1, a)) return false;
-    const int s = w ? tail_slot[1] : tail_slot[0];
-    zero_rows<DH>(tiles + s * TB, w ? tail_rows[1] : tail_rows[0]);
+  __device__ __forceinline__ void mend() {  // the oldest tail, which has arrived
+    const int s = int(notes & 255u), from = int((notes >> 8) & 255u);
+    zero_rows<DH>(tiles + s * TB, from);
     if ((threadIdx.x & 31) == 0) tc::arrive(full + 8 * s);
+    notes >>= 16;
     ++mended;
-    return true;
   }
   __device__ __forceinline__ bool mend_all() {
-    while (mended != tails)
-      if (!mend()) return false;
+    while (mended != tails) {
+      if (!wait(tail + 8 * (mended & 3u), mended >> 2, a)) return false;
+      mend();
+    }
+    return true;
+  }
+  // Waits for a barrier, mending meanwhile.
+  __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t phase) {
+    polls = 0;
+    while (mended != tails) {
+      if (__all_sync(0xffffffffu, tc::test(bar, phase & 1u))) return true;
+      if (__all_sync(0xffffffffu, tc::test(tail + 8 * (mended & 3u), (mended >> 2) & 1u))) mend();
+      else if (late()) return false;
+    }
+    return wait(bar, phase, a);
+  }
+  uint64_t since = 0;
+  uint32_t polls = 0;
+  __device__ __forceinline__ bool late() {  // the limit of wait_for's first loop
+    if ((++polls & 1023u) != 0) return false;
+    const uint64_t now = bulk::global_ns();
+    if (polls == 1024u) since = now;
+    if (!__any_sync(0xffffffffu, now - since > a.wait_ns)) return false;
+    if ((threadIdx.x & 31) == 0) set_err(a.err, FS_ERR_TIMEOUT);
     return true;
   }
   // The next tile: position y of head h of `map`, the first `valid` rows (of at most 128) the sample's.
@@ -320,23 +340,19 @@ struct Feeder {
   __device__ __forceinline__ bool put(const CUtensorMap* map, int h, int y, int valid, bool mend_tail) {
     const int lane = threadIdx.x & 31;
     const int s = int(slot % NS);
-    if (slot >= NS) {
-      const uint32_t phase = slot / NS - 1;
-      if (mended != tails && !__all_sync(0xffffffffu, bulk::try_wait(free + 8 * s, phase & 1u)) && !mend_all())
-        return false;
-      if (!wait(free + 8 * s, phase, a)) return false;
-    }
+    if (slot >= NS && !wait_for(free + 8 * s, slot / NS - 1)) return false;
     if (slot == 0 && a.skip_block == int64_t(blockIdx.x)) {
       ++slot;
       return true;
     }
     uint32_t bar = full + 8 * s;
     if (mend_tail && valid < kTile) {
-      if (tails - mended == 2 && !mend()) return false;
-      const uint32_t w = tails & 1u;
-      bar = tail + 8 * w;
-      if (w) tail_slot[1] = s, tail_rows[1] = valid;
-      else tail_slot[0] = s, tail_rows[0] = valid;
+      if (tails - mended == 4) {
+        if (!wait(tail + 8 * (mended & 3u), mended >> 2, a)) return false;
+        mend();
+      }
+      bar = tail + 8 * (tails & 3u);
+      notes |= uint64_t(uint32_t(s) | uint32_t(valid) << 8) << (16 * (tails - mended));
       ++tails;
     }
     if (lane == 0) {
@@ -348,12 +364,13 @@ struct Feeder {
   }
   // After a wait that gave up: every copy still in flight lands first.
   __device__ __forceinline__ void drain() {
-    for (uint32_t m = mended; m != tails; ++m) bulk::warp_wait(tail + 8 * (m & 1u), (m >> 1) & 1u, a.wait_ns);
-    for (uint32_t s = slot > NS ? slot - NS : 0; s < slot; ++s) {
-      bool tail_tile = false;
-      for (uint32_t m = mended; m != tails; ++m) tail_tile |= uint32_t((m & 1u) ? tail_slot[1] : tail_slot[0]) == s % NS;
-      if (!tail_tile) bulk::warp_wait(full + 8 * (s % NS), (s / NS) & 1u, a.wait_ns);
+    uint32_t tail_slots = 0;
+    for (uint32_t m = mended; m != tails; ++m, notes >>= 16) {
+      bulk::warp_wait(tail + 8 * (m & 3u), (m >> 2) & 1u, a.wait_ns);
+      tail_slots |= 1u << (notes & 31u);
     }
+    for (uint32_t s = slot > NS ? slot - NS : 0; s < slot; ++s)
+      if (!((tail_slots >> (s % NS)) & 1u)) bulk::warp_wait(full + 8 * (s % NS), (s / NS) & 1u, a.wait_ns);
   }
 };
 
@@ -580,17 +597,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
                                                                   int parts) {
   constexpr int TB = tile_bytes<DH>(), NS = fwd_slots<DH>();
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ __align__(8) uint64_t bars[12 + 2 * NS];
+  __shared__ __align__(8) uint64_t bars[13 + 2 * NS];
   __shared__ uint32_t tmem_at;
   __shared__ FwdUnit given[4];  // units handed over by the loading warp (no reader is two units behind)
   const uint32_t q_at = bulk::smem_addr(smem), kv_at = q_at + 2 * TB;
   const uint32_t bar = bulk::smem_addr(bars);
   const uint32_t q_full = bar, q_free = bar + 8, s_full = bar + 16, p_ready = bar + 32, o_full = bar + 48, tail = bar + 64,
-                 drain = bar + 80, full = bar + 96, free = full + 8 * NS;
+                 drain = bar + 96, full = bar + 104, free = full + 8 * NS;
   const int warp = int(tc::uni(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (warp == 8) {
     if (lane == 0) {
-      for (int i = 0; i < 12 + 2 * NS; ++i)
+      for (int i = 0; i < 13 + 2 * NS; ++i)
         bulk::mbar_init(bar + 8 * i, i == 1 ? 9 : (i == 4 || i == 5 ? 4 : 1));
       bulk::fence_init();
     }
@@ -626,7 +643,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
                  feed.put(&mv, f.kv_head, f.x.begin + at, f.x.L - at, true);
         };
         if (!(ok = put(0))) break;
-        if (k > 0 && !(ok = wait(q_free, k - 1, a))) break;
+        if (k > 0 && !(ok = feed.wait_for(q_free, k - 1))) break;
         if (lane == 0) {
           bulk::arrive_expect_tx(q_full, f.both ? 2 * TB : TB);
           load_tile<DH>(q_at, &mq, f.head0, f.x.begin + f.row0 * kTile, q_full);
@@ -634,7 +651,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
         }
         more = take.next();
         for (int j = 1; ok && j < f.n; ++j) ok = put(j);
-        if (!ok || !(ok = feed.mend_all())) break;
+        if (!ok) break;
       }
       if (ok && (ok = feed.mend_all() && (k == 0 || wait(q_free, k - 1, a))) && lane == 0) tc::arrive(q_full);
       if (!ok) {
@@ -858,19 +875,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                                                                  const __grid_constant__ CUtensorMap mdo, AttnArgs a) {
   constexpr int TB = tile_bytes<DH>(), NS = bwd_slots<DH>();
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ __align__(8) uint64_t bars[11 + 2 * NS];
+  __shared__ __align__(8) uint64_t bars[13 + 2 * NS];
   __shared__ uint32_t tmem_at;
   __shared__ DqUnit given[4];
   __shared__ float half_delta[2][kTile];
   const uint32_t q_at = bulk::smem_addr(smem), do_at = q_at + TB, kv_at = do_at + TB;
   const uint32_t bar = bulk::smem_addr(bars);
   const uint32_t q_full = bar, q_free = bar + 8, s_full = bar + 16, dp_full = bar + 24, s_read = bar + 32,
-                 ds_ready = bar + 40, delta_in = bar + 48, dq_full = bar + 56, tail = bar + 64, drain = bar + 80,
-                 full = bar + 88, free = full + 8 * NS;
+                 ds_ready = bar + 40, delta_in = bar + 48, dq_full = bar + 56, tail = bar + 64, drain = bar + 96,
+                 full = bar + 104, free = full + 8 * NS;
   const int warp = int(tc::uni(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (warp == 8) {
     if (lane == 0) {
-      for (int i = 0; i < 11 + 2 * NS; ++i) bulk::mbar_init(bar + 8 * i, i == 1 ? 9 : (i >= 4 && i <= 6 ? 8 : 1));
+      for (int i = 0; i < 13 + 2 * NS; ++i) bulk::mbar_init(bar + 8 * i, i == 1 ? 9 : (i >= 4 && i <= 6 ? 8 : 1));
       bulk::fence_init();
     }
     __syncwarp();
@@ -904,7 +921,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
       };
       const int at = f.x.begin + f.x.t * kTile;
       if (!(ok = (f.n == 1 || feed.put(&mo, f.head, at, kTile, false)) && put(0))) break;
-      if (k > 0 && !(ok = wait(q_free, k - 1, a))) break;
+      if (k > 0 && !(ok = feed.wait_for(q_free, k - 1))) break;
       if (lane == 0) {
         bulk::arrive_expect_tx(q_full, 2 * TB);
         load_tile<DH>(q_at, &mq, f.head, at, q_full);
@@ -912,9 +929,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
       }
       more = take.next();
       for (int j = 1; ok && j < f.n; ++j) ok = put(j);
-      if (!ok || !(ok = feed.mend_all())) break;
+      if (!ok) break;
     }
-    if (ok && (ok = k == 0 || wait(q_free, k - 1, a)) && lane == 0) tc::arrive(q_full);
+    if (ok && (ok = feed.mend_all() && (k == 0 || wait(q_free, k - 1, a))) && lane == 0) tc::arrive(q_full);
     if (!ok) {
       bulk::warp_wait(q_full, uint32_t(k) & 1u, a.wait_ns);
       feed.drain();
@@ -1143,19 +1160,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                                                                   const __grid_constant__ CUtensorMap mdo, AttnArgs a) {
   constexpr int TB = tile_bytes<DH>(), NS = bwd_slots<DH>();
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ __align__(8) uint64_t bars[11 + 2 * NS];
+  __shared__ __align__(8) uint64_t bars[13 + 2 * NS];
   __shared__ uint32_t tmem_at;
   __shared__ DkvUnit given[4];
   __shared__ __align__(16) float row_lse[2][kTile], row_delta[2][kTile];
   const uint32_t k_at = bulk::smem_addr(smem), v_at = k_at + TB, qd_at = v_at + TB;
   const uint32_t bar = bulk::smem_addr(bars);
   const uint32_t kv_full = bar, kv_free = bar + 8, s_full = bar + 16, dp_full = bar + 24, p_ready = bar + 32,
-                 ds_ready = bar + 40, rows_in = bar + 48, sums_full = bar + 56, tail = bar + 64, drain = bar + 80,
-                 full = bar + 88, free = full + 8 * NS;
+                 ds_ready = bar + 40, rows_in = bar + 48, sums_full = bar + 56, tail = bar + 64, drain = bar + 96,
+                 full = bar + 104, free = full + 8 * NS;
   const int warp = int(tc::uni(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (warp == 8) {
     if (lane == 0) {
-      for (int i = 0; i < 11 + 2 * NS; ++i) bulk::mbar_init(bar + 8 * i, i == 1 ? 9 : (i >= 4 && i <= 6 ? 8 : 1));
+      for (int i = 0; i < 13 + 2 * NS; ++i) bulk::mbar_init(bar + 8 * i, i == 1 ? 9 : (i >= 4 && i <= 6 ? 8 : 1));
       bulk::fence_init();
     }
     __syncwarp();
@@ -1190,7 +1207,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
         return fine;
       };
       if (!(ok = put())) break;
-      if (k > 0 && !(ok = wait(kv_free, k - 1, a))) break;
+      if (k > 0 && !(ok = feed.wait_for(kv_free, k - 1))) break;
       if (lane == 0) {
         bulk::arrive_expect_tx(kv_full, 2 * TB);
         load_tile<DH>(k_at, &mk, f.kv_head, f.x.begin + f.x.t * kTile, kv_full);
@@ -1198,9 +1215,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
       }
       more = take.next();
       for (int j = 1; ok && j < f.n; ++j) ok = put();
-      if (!ok || !(ok = feed.mend_all())) break;
+      if (!ok) break;
     }
-    if (ok && (ok = k == 0 || wait(kv_free, k - 1, a)) && lane == 0) tc::arrive(kv_full);
+    if (ok && (ok = feed.mend_all() && (k == 0 || wait(kv_free, k - 1, a))) && lane == 0) tc::arrive(kv_full);
     if (!ok) {
       bulk::warp_wait(kv_full, uint32_t(k) & 1u, a.wait_ns);
       feed.drain();
@@ -1357,25 +1374,31 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
       if (x.split >= 0) {
         const int64_t unit = int64_t(x.split) * a.kv_heads + f.kv_head;
         float4* both = reinterpret_cast<float4*>(a.partial) + (unit * 8 + warp) * (2 * DH * 8);
-        float4* mine = both + x.part * (DH * 8);
+        int32_t* flag = a.flags + unit * 8 + warp;
+        // is the other half's share there?  If not, leave this one's, and ask again
+        int32_t came = 0;
+        if (lane == 0) came = *reinterpret_cast<volatile int32_t*>(flag);
+        came = __shfl_sync(0xffffffffu, came, 0);
+        if (came == 0) {
+          float4* mine = both + x.part * (DH * 8);
 #pragma unroll
-        for (int b = 0; b < DH / 32; ++b) {
-          float g[32];
-          tc::ld32(from + 32 * b, g);
-          tc::wait_ld();
-          tc::tie32(g);
+          for (int b = 0; b < DH / 32; ++b) {
+            float g[32];
+            tc::ld32(from + 32 * b, g);
+            tc::wait_ld();
+            tc::tie32(g);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            __stcg(mine + (b * 8 + i) * 32 + lane, make_float4(g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]));
-        }
-        __threadfence();
-        __syncwarp();
-        int32_t first = 0;
-        if (lane == 0) first = atomicAdd(a.flags + unit * 8 + warp, 1);
-        first = __shfl_sync(0xffffffffu, first, 0);
-        if (first == 0) {
-          tc::fence_before();
-          continue;  // the other half adds them up
+            for (int i = 0; i < 8; ++i)
+              __stcg(mine + (b * 8 + i) * 32 + lane, make_float4(g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]));
+          }
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) came = atomicAdd(flag, 1);
+          came = __shfl_sync(0xffffffffu, came, 0);
+          if (came == 0) {
+            tc::fence_before();
+            continue;  // the other half adds them up
+          }
         }
         __threadfence();
         other = both + (1 - x.part) * (DH * 8);
