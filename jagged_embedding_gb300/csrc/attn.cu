@@ -440,36 +440,35 @@ struct Taker {
   }
 };
 
-// D[128 x 128] = A B^T over DH columns, both tiles K-major.  Called by a whole warp; lane 0 issues.
+// The products are issued by one thread in batches: what one batch waits for and
+// the descriptors of its operands are found before, by the whole warp, so that between two products
+// of a batch there is nothing but the products (a few dozen instructions of one warp
+// beside sixteen busy ones take longer than the queue of products lasts).
+
+// D[128 x 128] = A B^T over DH columns, both tiles K-major: descriptors of tc::desc_k.
 template <int DH>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b) {
   constexpr uint32_t id = tc::idesc(kTile, kTile, false);
-  const uint32_t da = tc::desc_k(a), db = tc::desc_k(tc::uni(b));
-  if ((threadIdx.x & 31) == 0) {
-    tc::mma_ss<true>(d, tc::at(da, 0), tc::at(db, 0), id, false);
+  tc::mma_ss<true>(d, tc::at(a, 0), tc::at(b, 0), id, false);
 #pragma unroll
-    for (int k = 1; k < DH / 16; ++k) {
-      const uint32_t off = (k / 4) * kBox + (k % 4) * 32;
-      tc::mma_ss<false>(d, tc::at(da, off), tc::at(db, off), id, true);
-    }
+  for (int k = 1; k < DH / 16; ++k) {
+    const uint32_t off = (k / 4) * kBox + (k % 4) * 32;
+    tc::mma_ss<false>(d, tc::at(a, off), tc::at(b, off), id, true);
   }
 }
 
 // D[128 x DH] (+)= A B, A [128 x 128] bf16 in tensor memory, its first 64 columns at a0, the
-// others at a1, B a tile of 128 rows.  Called by a whole warp; lane 0 issues.
+// others at a1, B a tile of 128 rows: a descriptor of tc::desc_mn.
 template <int DH>
 __device__ __forceinline__ void mma_cols(uint32_t d, uint32_t a0, uint32_t a1, uint32_t b, bool acc) {
   constexpr uint32_t id = tc::idesc(kTile, DH, true);
-  const uint32_t db = tc::desc_mn(tc::uni(b), kBox);
-  if ((threadIdx.x & 31) == 0) {
-    tc::mma_ts<true>(d, a0, tc::at(db, 0), id, acc);
+  tc::mma_ts<true>(d, a0, tc::at(b, 0), id, acc);
 #pragma unroll
-    for (int k = 1; k < kTile / 16; ++k)
-      tc::mma_ts<false>(d, (k < 4 ? a0 + 8 * k : a1 + 8 * (k - 4)), tc::at(db, k * 2048), id, true);
-  }
+  for (int k = 1; k < kTile / 16; ++k)
+    tc::mma_ts<false>(d, (k < 4 ? a0 + 8 * k : a1 + 8 * (k - 4)), tc::at(b, k * 2048), id, true);
 }
 
-// Commit by the lane that issues the products.
+// Commit by the issuing lane of a whole warp.
 __device__ __forceinline__ void commit(uint32_t bar) {
   if ((threadIdx.x & 31) == 0) tc::commit(bar);
 }
@@ -661,6 +660,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
     } else if (warp == 8) {
       // products: at step j, o += p v of key tile j - 1 and x of key tile j, of query tile 0, then of 1
       // (one issuing thread: two would fall into step, and both tiles' softmax would wait together)
+      const uint32_t q_desc = tc::desc_k(q_at);
       Place<NS> ks(0), vs(1);
       uint32_t done[2] = {0, 0};  // p's consumed
       bool ok = true;
@@ -674,35 +674,43 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
           const Place<NS> v = vs, key = ks;
           if (j > 0) vs.skip(2);
           ks.skip(2);
+          const uint32_t v_desc = tc::uni(tc::desc_mn(kv_at + v.s * TB, kBox)), k_desc = tc::uni(tc::desc_k(kv_at + key.s * TB));
+          const uint32_t v_free = tc::uni(free + 8 * v.s), k_free = tc::uni(free + 8 * key.s);
+          if (j == f.n && !(ok = wait(full + 8 * v.s, v.phase, a))) break;  // (the last may be mended)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            // while the first tile's products run: this step's value tile is there for both; the next
-            // step's tiles are looked for before the second tile's
+            // while the first tile's products run, the next step's tiles are looked for
             if (i == 1 && j + 1 < f.n && !(ok = wait(full + 8 * vs.s, vs.phase, a) && wait(full + 8 * ks.s, ks.phase, a)))
               break;
-            if (i == 0 && j == f.n && !(ok = wait(full + 8 * v.s, v.phase, a))) break;  // (the last may be mended)
-            if (i == 1 && !f.both) continue;
-            if (j > 0 && f.meets(i, j - 1)) {
-              if (!(ok = wait(p_ready + 8 * i, done[i], a))) break;
-              ++done[i];
-              tc::fence_after();
-              mma_cols<DH>(o_at + DH * i, s_at + 128 * i, s_at + 128 * i + 32, kv_at + v.s * TB, acc[i]);
-              acc[i] = true;
+            const bool there = i == 0 || f.both;
+            const bool pv = there && j > 0 && f.meets(i, j - 1), qk = there && j < f.n && f.meets(i, j);
+            if (pv && !(ok = wait(p_ready + 8 * i, done[i], a))) break;
+            if (lane == 0) {
+              if (pv) {
+                tc::fence_after();
+                mma_cols<DH>(o_at + DH * i, s_at + 128 * i, s_at + 128 * i + 32, v_desc, acc[i]);
+              }
+              if (qk) {  // x overwrites p: the products execute in the order they are issued
+                mma_rows<DH>(s_at + 128 * i, q_desc + i * (TB >> 4), k_desc);
+                tc::commit(s_full + 8 * i);
+              }
+              if (i == 1) {
+                if (j > 0) tc::commit(v_free);
+                if (j < f.n) tc::commit(k_free);
+                if (j == f.n - 1) tc::commit(q_free);
+                if (j == f.n) {  // (a barrier for each: a warpgroup without work would fall phases behind one of both)
+                  tc::commit(o_full);
+                  if (f.both) tc::commit(o_full + 8);
+                }
+              }
             }
-            if (j < f.n && f.meets(i, j)) {
-              // x overwrites p: the products execute in the order they are issued
-              mma_rows<DH>(s_at + 128 * i, q_at + i * TB, kv_at + key.s * TB);
-              commit(s_full + 8 * i);
+            __syncwarp();
+            if (pv) {
+              ++done[i];
+              acc[i] = true;
             }
           }
           if (!ok) break;
-          if (j > 0) commit(free + 8 * v.s);
-          if (j < f.n) commit(free + 8 * key.s);
-          if (j == f.n - 1) commit(q_free);
-          if (j == f.n) {  // (a barrier for each: a warpgroup without work would fall phases behind one of both)
-            commit(o_full);
-            if (f.both) commit(o_full + 8);
-          }
         }
         ks.back(2);  // (the last step has no key tile)
       }
@@ -938,44 +946,59 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
     }
   } else if (warp == 8) {
     Place<NS> ks(0), vs(1), kq(0);  // next key and value tile to read, and the key tile of the next dq product
+    const uint32_t q_desc = tc::desc_k(q_at), do_desc = tc::desc_k(do_at);
     uint32_t c = 0;                 // key tiles so far
     bool ok = true;
     auto scores = [&]() {           // x of the next key tile, into columns that the last tile's readers have left
+      const uint32_t k_desc = tc::uni(tc::desc_k(kv_at + ks.s * TB));
       if (!wait(full + 8 * ks.s, ks.phase, a) || (c > 0 && !wait(s_read, c - 1, a))) return false;
-      tc::fence_after();
-      mma_rows<DH>(s_at, q_at, kv_at + ks.s * TB);
-      commit(s_full);
+      if (lane == 0) {
+        tc::fence_after();
+        mma_rows<DH>(s_at, q_desc, k_desc);
+        tc::commit(s_full);
+      }
+      __syncwarp();
       ks.skip(2);
       return true;
     };
-    auto products = [&]() {  // do v^T of the next value tile, over ds: the products execute in the order they are issued
-      mma_rows<DH>(dp_at, do_at, kv_at + vs.s * TB);
-      commit(dp_full);
-      commit(free + 8 * vs.s);
-      vs.skip(2);
+    // dq of the last ds (where `sum`), then do v^T of the next value tile over it (where `more`): the products
+    // execute in the order they are issued
+    auto sums_and_products = [&](bool sum, bool acc, bool more) {
+      const uint32_t kq_desc = tc::uni(tc::desc_mn(kv_at + kq.s * TB, kBox)), v_desc = tc::uni(tc::desc_k(kv_at + vs.s * TB));
+      const uint32_t k_free = tc::uni(free + 8 * kq.s), v_free = tc::uni(free + 8 * vs.s);
+      if (more && !wait(full + 8 * vs.s, vs.phase, a)) return false;
+      if (sum && !wait(ds_ready, c - 1, a)) return false;
+      if (lane == 0) {
+        tc::fence_after();
+        if (sum) {
+          mma_cols<DH>(dq_at, dp_at, dp_at + 64, kq_desc, acc);
+          tc::commit(k_free);
+        }
+        if (more) {
+          mma_rows<DH>(dp_at, do_desc, v_desc);
+          tc::commit(dp_full);
+          tc::commit(v_free);
+        } else {
+          tc::commit(dq_full);
+        }
+      }
+      __syncwarp();
+      if (sum) kq.skip(2);
+      if (more) vs.skip(2);
+      return true;
     };
     for (int k = 0; ok; ++k) {
       if (!(ok = wait(q_full, k, a))) break;
       const int n = int(tc::uni(uint32_t(given[k & 3].n)));
       if (n < 0) break;
       if (n > 1) ks.skip(1), vs.skip(1), kq.skip(1);  // (the tile of out)
-      if (!(ok = scores() && wait(full + 8 * vs.s, vs.phase, a))) break;
-      products();
+      if (!(ok = scores() && sums_and_products(false, false, true))) break;
       for (int j = 0; j < n; ++j) {
         ++c;
-        if (j + 1 < n) {
-          if (!(ok = scores() && wait(full + 8 * vs.s, vs.phase, a))) break;
-        } else {
-          commit(q_free);
-        }
-        if (!(ok = wait(ds_ready, c - 1, a))) break;
-        tc::fence_after();
-        mma_cols<DH>(dq_at, dp_at, dp_at + 64, kv_at + kq.s * TB, j != 0);
-        commit(free + 8 * kq.s);
-        kq.skip(2);
-        if (j + 1 < n) products();
+        if (j + 1 == n) commit(q_free);
+        else if (!(ok = scores())) break;
+        if (!(ok = sums_and_products(true, j != 0, j + 1 < n))) break;
       }
-      if (ok) commit(dq_full);
     }
     if (!ok) {
       commit(drain);
@@ -1225,48 +1248,60 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
   } else if (warp == 8) {
     Place<NS> qs(0), ds(1);  // tiles of the next x and v do^T
     Place<NS> qk(0), dv(1);  // tiles of the next dk and dv products
+    const uint32_t k_desc = tc::desc_k(k_at), v_desc = tc::desc_k(v_at);
     uint32_t c = 0;          // query tiles so far
     bool ok = true;
-    // x^T overwrites p^T, v do^T overwrites ds^T: the products execute in the order they are issued
-    auto scores = [&]() {
-      mma_rows<DH>(s_at, k_at, qd_at + qs.s * TB);
-      commit(s_full);
-      qs.skip(2);
-    };
-    auto products = [&]() {
-      mma_rows<DH>(dp_at, v_at, qd_at + ds.s * TB);
-      commit(dp_full);
-      ds.skip(2);
-    };
     for (int k = 0; ok; ++k) {
       if (!(ok = wait(kv_full, k, a))) break;
       const int n = int(tc::uni(uint32_t(given[k & 3].n)));
       if (n < 0) break;
-      if (!(ok = wait(full + 8 * qs.s, qs.phase, a))) break;
-      scores();
-      if (!(ok = wait(full + 8 * ds.s, ds.phase, a))) break;
-      products();
-      if (n == 1) commit(kv_free);
-      for (int j = 0; j < n; ++j, ++c) {
-        if (j + 1 < n && !(ok = wait(full + 8 * qs.s, qs.phase, a))) break;
-        if (!(ok = wait(p_ready, c, a))) break;
-        tc::fence_after();
-        mma_cols<DH>(dv_at, s_at, s_at + 64, qd_at + dv.s * TB, j != 0);
-        commit(free + 8 * dv.s);
-        dv.skip(2);
-        if (j + 1 < n) {
-          scores();
-          if (!(ok = wait(full + 8 * ds.s, ds.phase, a))) break;
+      // step -1 has the first tile's x^T and v do^T alone; step j dv and dk of tile j and the next tile's; x^T
+      // overwrites p^T, v do^T overwrites ds^T: the products execute in the order they are issued
+      for (int j = -1; j < n; ++j) {
+        const bool sum = j >= 0, more = j + 1 < n;
+        {
+          const uint32_t do_desc = tc::uni(tc::desc_mn(qd_at + dv.s * TB, kBox)), q_desc = tc::uni(tc::desc_k(qd_at + qs.s * TB));
+          const uint32_t do_free = tc::uni(free + 8 * dv.s);
+          if (more && !(ok = wait(full + 8 * qs.s, qs.phase, a))) break;
+          if (sum && !(ok = wait(p_ready, c, a))) break;
+          if (lane == 0) {
+            tc::fence_after();
+            if (sum) {
+              mma_cols<DH>(dv_at, s_at, s_at + 64, do_desc, j != 0);
+              tc::commit(do_free);
+            }
+            if (more) {
+              mma_rows<DH>(s_at, k_desc, q_desc);
+              tc::commit(s_full);
+            }
+          }
+          __syncwarp();
         }
-        if (!(ok = wait(ds_ready, c, a))) break;
-        tc::fence_after();
-        mma_cols<DH>(dk_at, dp_at, dp_at + 64, qd_at + qk.s * TB, j != 0);
-        commit(free + 8 * qk.s);
-        qk.skip(2);
-        if (j + 1 < n) products();
-        if (j + 2 == n) commit(kv_free);
+        const uint32_t q_desc = tc::uni(tc::desc_mn(qd_at + qk.s * TB, kBox)), do_desc = tc::uni(tc::desc_k(qd_at + ds.s * TB));
+        const uint32_t q_free = tc::uni(free + 8 * qk.s);
+        if (more && !(ok = wait(full + 8 * ds.s, ds.phase, a))) break;
+        if (sum && !(ok = wait(ds_ready, c, a))) break;
+        if (lane == 0) {
+          tc::fence_after();
+          if (sum) {
+            mma_cols<DH>(dk_at, dp_at, dp_at + 64, q_desc, j != 0);
+            tc::commit(q_free);
+          }
+          if (more) {
+            mma_rows<DH>(dp_at, v_desc, do_desc);
+            tc::commit(dp_full);
+            if (j + 2 == n) tc::commit(kv_free);
+          } else {
+            tc::commit(sums_full);
+          }
+        }
+        __syncwarp();
+        if (sum) {
+          dv.skip(2), qk.skip(2);
+          ++c;
+        }
+        if (more) qs.skip(2), ds.skip(2);
       }
-      if (ok) commit(sums_full);
     }
     if (!ok) {
       commit(drain);
