@@ -468,6 +468,18 @@ __device__ __forceinline__ void mma_cols(uint32_t d, uint32_t a0, uint32_t a1, u
     tc::mma_ts<false>(d, (k < 4 ? a0 + 8 * k : a1 + 8 * (k - 4)), tc::at(b, k * 2048), id, true);
 }
 
+// The same from shared-memory addresses, called by a whole warp.
+template <int DH>
+__device__ __forceinline__ void warp_mma_rows(uint32_t d, uint32_t a, uint32_t b) {
+  const uint32_t da = tc::desc_k(a), db = tc::desc_k(tc::uni(b));
+  if ((threadIdx.x & 31) == 0) mma_rows<DH>(d, da, db);
+}
+template <int DH>
+__device__ __forceinline__ void warp_mma_cols(uint32_t d, uint32_t a0, uint32_t a1, uint32_t b, bool acc) {
+  const uint32_t db = tc::desc_mn(tc::uni(b), kBox);
+  if ((threadIdx.x & 31) == 0) mma_cols<DH>(d, a0, a1, db, acc);
+}
+
 // Commit by the issuing lane of a whole warp.
 __device__ __forceinline__ void commit(uint32_t bar) {
   if ((threadIdx.x & 31) == 0) tc::commit(bar);
@@ -650,7 +662,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
         }
         more = take.next();
         for (int j = 1; ok && j < f.n; ++j) ok = put(j);
-        if (!ok) break;
+        if (!ok || !(ok = feed.mend_all())) break;
       }
       if (ok && (ok = feed.mend_all() && (k == 0 || wait(q_free, k - 1, a))) && lane == 0) tc::arrive(q_full);
       if (!ok) {
@@ -660,7 +672,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
     } else if (warp == 8) {
       // products: at step j, o += p v of key tile j - 1 and x of key tile j, of query tile 0, then of 1
       // (one issuing thread: two would fall into step, and both tiles' softmax would wait together)
-      const uint32_t q_desc = tc::desc_k(q_at);
       Place<NS> ks(0), vs(1);
       uint32_t done[2] = {0, 0};  // p's consumed
       bool ok = true;
@@ -674,43 +685,35 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
           const Place<NS> v = vs, key = ks;
           if (j > 0) vs.skip(2);
           ks.skip(2);
-          const uint32_t v_desc = tc::uni(tc::desc_mn(kv_at + v.s * TB, kBox)), k_desc = tc::uni(tc::desc_k(kv_at + key.s * TB));
-          const uint32_t v_free = tc::uni(free + 8 * v.s), k_free = tc::uni(free + 8 * key.s);
-          if (j == f.n && !(ok = wait(full + 8 * v.s, v.phase, a))) break;  // (the last may be mended)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            // while the first tile's products run, the next step's tiles are looked for
+            // while the first tile's products run: this step's value tile is there for both; the next
+            // step's tiles are looked for before the second tile's
             if (i == 1 && j + 1 < f.n && !(ok = wait(full + 8 * vs.s, vs.phase, a) && wait(full + 8 * ks.s, ks.phase, a)))
               break;
-            const bool there = i == 0 || f.both;
-            const bool pv = there && j > 0 && f.meets(i, j - 1), qk = there && j < f.n && f.meets(i, j);
-            if (pv && !(ok = wait(p_ready + 8 * i, done[i], a))) break;
-            if (lane == 0) {
-              if (pv) {
-                tc::fence_after();
-                mma_cols<DH>(o_at + DH * i, s_at + 128 * i, s_at + 128 * i + 32, v_desc, acc[i]);
-              }
-              if (qk) {  // x overwrites p: the products execute in the order they are issued
-                mma_rows<DH>(s_at + 128 * i, q_desc + i * (TB >> 4), k_desc);
-                tc::commit(s_full + 8 * i);
-              }
-              if (i == 1) {
-                if (j > 0) tc::commit(v_free);
-                if (j < f.n) tc::commit(k_free);
-                if (j == f.n - 1) tc::commit(q_free);
-                if (j == f.n) {  // (a barrier for each: a warpgroup without work would fall phases behind one of both)
-                  tc::commit(o_full);
-                  if (f.both) tc::commit(o_full + 8);
-                }
-              }
-            }
-            __syncwarp();
-            if (pv) {
+            if (i == 0 && j == f.n && !(ok = wait(full + 8 * v.s, v.phase, a))) break;  // (the last may be mended)
+            if (i == 1 && !f.both) continue;
+            if (j > 0 && f.meets(i, j - 1)) {
+              if (!(ok = wait(p_ready + 8 * i, done[i], a))) break;
               ++done[i];
+              tc::fence_after();
+              warp_mma_cols<DH>(o_at + DH * i, s_at + 128 * i, s_at + 128 * i + 32, kv_at + v.s * TB, acc[i]);
               acc[i] = true;
+            }
+            if (j < f.n && f.meets(i, j)) {
+              // x overwrites p: the products execute in the order they are issued
+              warp_mma_rows<DH>(s_at + 128 * i, q_at + i * TB, kv_at + key.s * TB);
+              commit(s_full + 8 * i);
             }
           }
           if (!ok) break;
+          if (j > 0) commit(free + 8 * v.s);
+          if (j < f.n) commit(free + 8 * key.s);
+          if (j == f.n - 1) commit(q_free);
+          if (j == f.n) {  // (a barrier for each: a warpgroup without work would fall phases behind one of both)
+            commit(o_full);
+            if (f.both) commit(o_full + 8);
+          }
         }
         ks.back(2);  // (the last step has no key tile)
       }
