@@ -31,6 +31,15 @@ op is one of
   autotune  -- VBS AutoTune with T samples over R logical ranks (lognormal(7, 1.6) lengths up to 16384,
                alpha 1.5, length-sorted cut): fs_vbs_autotune, fs_balance_vbs_tuned and the plain
                fs_balance_vbs, each timed alone (median of reps calls, CUDA events)
+  lookup    -- fs_emb_lookup_scaled of T bounded-Zipf(1.0) IDs over R bf16 rows of 128, bf16 out
+  row-grads -- fs_emb_grad_rows of the same IDs, bf16 dout rows of 128, f32 gradients
+  norm      -- fs_rmsnorm of T bf16 rows of R columns with the residual's addition, 8-bit output
+  norm-backward -- fs_rmsnorm_backward of T bf16 rows of R columns with the residual stream's gradient
+  attention -- fs_jagged_attn, causal, T positions in samples of lognormal(6.5, 1.5) lengths up to R with 32
+               candidates each (fewer in shorter ones), 8 query and 2 key/value heads of 128
+  attention-backward -- fs_jagged_attn_backward on the same batch
+  (these six print the median time and the bandwidth of their algorithmic bytes, the last two also the rate of
+  the products over visible pairs)
 Inputs come from jagged_embedding_gb300.synthetic; every call goes through the C ABI.
 Exits non-zero if a call reports an error.
 """
@@ -49,11 +58,13 @@ from jagged_embedding_gb300 import synthetic  # noqa: E402
 
 DIM = 64
 SHARDS = 256
+SEQUENCE_OPS = ("lookup", "row-grads", "norm", "norm-backward", "attention", "attention-backward")
 
 
 def main(argv) -> int:
     if len(argv) < 3 or argv[0] not in ("gather", "backward", "backward-bf16", "bucketize", "transpose",
-                                        "autotune", "gather-sorted", "prep", "sorted-step", "bitmap", "collision"):
+                                        "autotune", "gather-sorted", "prep", "sorted-step", "bitmap", "collision",
+                                        *SEQUENCE_OPS):
         print(__doc__)
         return 2
     op, T, R = argv[0], int(argv[1]), int(argv[2])
@@ -69,6 +80,8 @@ def main(argv) -> int:
         return _autotune(T, R, reps, dev, g, err)
     if op == "prep":
         return _prep(T, R, reps, dev, g, err)
+    if op in SEQUENCE_OPS:
+        return _sequence(op, T, R, reps, dev, g, err)
     ids = synthetic.zipf_rows(R, 1.0, T, g, dev)
     if op == "sorted-step":
         return _sorted_step(ids, T, R, reps, dev, g, err)
@@ -269,6 +282,66 @@ def _autotune(S, n, reps, dev, g, err):
     B.check(err, "autotune")
     print(f"autotune S={S} n={n}: update {1000 * t_upd:.1f} us, tuned VBS cut {1000 * t_tuned:.1f} us, "
           f"plain VBS cut {1000 * t_plain:.1f} us (median of {reps})")
+    return 0
+
+
+def _sequence(op, T, R, reps, dev, g, err):
+    reps = max(reps, 5)
+    bf = torch.bfloat16
+    flops = 0
+    if op in ("lookup", "row-grads"):
+        ids = synthetic.zipf_rows(R, 1.0, T, g, dev)
+        distinct = ids.unique().numel()
+        if op == "lookup":
+            table = torch.randn(R, 128, device=dev, generator=g).to(bf)
+            out = torch.empty(T, 128, dtype=bf, device=dev)
+            fn = lambda: B.fs_emb_lookup_scaled(table, ids, 8.0, out=out, err=err)  # noqa: E731
+            nbytes = T * (8 + 256) + distinct * 256
+        else:
+            dout = torch.randn(T, 128, device=dev, generator=g).to(bf)
+            rows, grads, count, _ = B.fs_emb_grad_rows(ids, dout, R, err=err)
+            ws = B.workspace(B.emb_grad_rows_workspace_size(T, R, 128), dev)
+            fn = lambda: B.fs_emb_grad_rows(ids, dout, R, rows=rows, row_grads=grads, count=count, err=err,  # noqa: E731
+                                            ws=ws)
+            nbytes = T * (8 + 256) + distinct * (8 + 512)
+    elif op in ("norm", "norm-backward"):
+        x, res, dy = (torch.randn(T, R, device=dev, generator=g).to(bf) for _ in range(3))
+        gamma = torch.ones(R, device=dev)
+        q, scale, h, rstd = B.fs_rmsnorm(x, gamma, 1e-6, res=res, y_dtype=torch.float8_e4m3fn)
+        if op == "norm":
+            fn = lambda: B.fs_rmsnorm(x, gamma, 1e-6, res=res, sum_out=h, y=q, y_scale=scale, rstd=rstd)  # noqa: E731
+            nbytes = T * (R * 7 + 8)
+        else:
+            dh, dg = torch.empty_like(h), torch.empty(R, device=dev)
+            ws = B.workspace(B.rmsnorm_backward_workspace_size(T, R), dev)
+            fn = lambda: B.fs_rmsnorm_backward(dy, h, gamma, rstd, dsum=res, dh=dh, dgamma=dg, ws=ws)  # noqa: E731
+            nbytes = T * (R * 8 + 4)
+    else:
+        H, Hkv, Dh = 8, 2, 128
+        L = torch.empty(T // 8 + 1, dtype=torch.float64, device=dev).log_normal_(6.5, 1.5, generator=g)
+        L = L.round().clamp_(1, R).long().cumsum(0)
+        off = torch.cat([torch.zeros(1, dtype=torch.int64, device=dev), L[L < T], torch.full((1,), T, device=dev)])
+        n = off[1:] - off[:-1]
+        cand = n.clamp(max=32).to(torch.int32)
+        u, c = (n - cand).double(), cand.double()
+        pairs = float((u * (u + 1) / 2 + c * (u + 1)).sum()) * H
+        q, k, v = torch.randn(T, H + 2 * Hkv, Dh, device=dev, generator=g).to(bf).split([H, Hkv, Hkv], dim=1)
+        ws = B.workspace(B.jagged_attn_workspace_size(T, n.numel(), H, Hkv, Dh), dev)
+        out, lse, _ = B.fs_jagged_attn(q, k, v, off, Dh ** -0.5, cand_len=cand, err=err, ws=ws)
+        if op == "attention":
+            fn = lambda: B.fs_jagged_attn(q, k, v, off, Dh ** -0.5, cand_len=cand, out=out, lse=lse, err=err,  # noqa: E731
+                                          ws=ws)
+            nbytes, flops = T * (2 * Dh * 2 * (H + Hkv) + 4 * H), 4 * Dh * pairs
+        else:
+            dout = torch.randn(T, H, Dh, device=dev, generator=g).to(bf)
+            d = B.fs_jagged_attn_backward(q, k, v, out, lse, dout, off, Dh ** -0.5, cand_len=cand, err=err, ws=ws)
+            fn = lambda: B.fs_jagged_attn_backward(q, k, v, out, lse, dout, off, Dh ** -0.5, cand_len=cand,  # noqa: E731
+                                                   dq=d[0], dk=d[1], dv=d[2], err=err, ws=ws)
+            nbytes, flops = T * (2 * Dh * 4 * (H + Hkv) + 4 * H), 10 * Dh * pairs
+    t = _median_ms(fn, reps)
+    B.check(err, op)
+    rate = f", {flops / t / 1e9:.0f} TFLOP/s" if flops else ""
+    print(f"{op} T={T} R={R}: {1000 * t:.1f} us, {nbytes / t / 1e6:.0f} GB/s{rate} (median of {reps})")
     return 0
 
 
