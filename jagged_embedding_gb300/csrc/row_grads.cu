@@ -4,14 +4,14 @@
 // optimizer: what update_embedding receives, for callers that clip, average or
 // apply an optimizer of their own.
 //
-//   1. sort of (row, position): the library's radix passes;
-//   2. heads: numbers the distinct rows of the sorted entries (single-pass scan);
+//   1. sort of (row, position): counting passes over one range of entries a block;
+//   2. heads: numbers the distinct rows of the sorted entries, over the same ranges;
 //   3. reduce: a group of lanes per tile of `chunk` sorted entries sums dout
 //      rows in fp32 in entry order; a row inside the tile is written out, a row
 //      that crosses a tile's edge leaves partial sums;
 //   4. join: adds the partial sums of the rows that cross edges, in tile order
 //      (a hot row crosses thousands of tiles: a whole block adds those).
-// A small batch (at most 8192 entries) takes two launches instead of sixteen: one block sorts and
+// A small batch (at most 8192 entries) takes two launches instead of ten to sixteen: one block sorts and
 // numbers in shared memory, then a warp sums each distinct row.
 // The order of every sum follows from the sorted order and T alone: results are
 // the same bits from run to run.
@@ -22,37 +22,12 @@
 
 #include "convert.cuh"
 #include "fs_common.cuh"
-#include "radix.cuh"
+#include "range_sort.cuh"
 
 namespace fs {
 namespace {
 
-struct SrcIds {
-  using Key = uint32_t;
-  static constexpr bool kIndexValue = true;  // value = item index
-  static constexpr bool kFetch2 = false;
-  const int64_t* ids;
-  int64_t R;
-  using Raw = int64_t;
-  template <bool>
-  __device__ __forceinline__ Raw fetch(int64_t i) const { return __ldcs(ids + i); }
-  __device__ __forceinline__ bool make(Raw id, int64_t i, int, Key& key, uint32_t& val, int32_t* err) const {
-    if (uint64_t(id) >= uint64_t(R)) {
-      if (err) set_err(err, FS_ERR_ID_RANGE);
-      return false;
-    }
-    key = uint32_t(id);
-    val = uint32_t(i);
-    return true;
-  }
-  __device__ __forceinline__ uint32_t digit(Key key, int shift, int bits, int) const {
-    return (key >> shift) & ((1u << bits) - 1u);
-  }
-};
-
 // ------------------------------------------------------------- numbering the rows
-
-constexpr int kHeadThreads = 256, kHeadItems = 8, kHeadTile = kHeadThreads * kHeadItems;
 
 struct Numbering {
   int64_t* rows;    // [cap] out
@@ -63,59 +38,75 @@ struct Numbering {
   int chunk_log2;
 };
 
-__global__ void __launch_bounds__(kHeadThreads) heads_kernel(const uint32_t* __restrict__ keys, const int64_t* n_dev,
-                                                             Numbering N, uint64_t* status, uint32_t* ticket,
-                                                             int32_t* err, int64_t limit) {
-  __shared__ uint32_t scan[32];
-  __shared__ int64_t s_tile;
-  __shared__ uint64_t s_excl;
-  if (threadIdx.x == 0) s_tile = atomicAdd(ticket, 1u);  // tiles in the order blocks start: the look-back never waits for a block not yet running
-  __syncthreads();
-  const int64_t n = *n_dev, tile = s_tile;
-  const int64_t ntiles = (n + kHeadTile - 1) / kHeadTile;
-  if (tile >= ntiles) {
-    if (n == 0 && tile == 0 && threadIdx.x == 0) {
-      *N.count = 0;
-      N.start[0] = 0;
+// Distinct rows that begin in each block's range of the sorted entries, then their numbers:
+// a block adds up the counts of the blocks before it (two launches, 8 B read per entry).
+constexpr int kHeadThreads = range_sort::kThreads, kHeadItems = 8, kHeadTile = kHeadThreads * kHeadItems;
+
+__global__ void __launch_bounds__(kHeadThreads) head_count_kernel(const uint32_t* keys, const int64_t* n_dev,
+                                                                  uint32_t* __restrict__ counts) {
+  __shared__ uint32_t scratch[32];
+  range_sort::launch_next();
+  range_sort::wait_previous();
+  const range_sort::Range r = range_sort::range_of(__ldcg(n_dev));
+  uint32_t mine = 0, total;
+  for (int64_t j = threadIdx.x; j < r.count; j += kHeadTile) {
+    uint32_t k[kHeadItems], p[kHeadItems];
+#pragma unroll
+    for (int q = 0; q < kHeadItems; ++q)
+      if (j + q * kHeadThreads < r.count) {
+        const int64_t i = r.first + j + q * kHeadThreads;
+        k[q] = __ldcg(keys + i);
+        p[q] = i ? __ldcg(keys + i - 1) : ~k[q];
+      }
+#pragma unroll
+    for (int q = 0; q < kHeadItems; ++q) mine += j + q * kHeadThreads < r.count && k[q] != p[q];
+  }
+  block_exclusive_scan<uint32_t>(mine, scratch, &total);
+  if (threadIdx.x == 0) counts[blockIdx.x] = total;
+}
+
+__global__ void __launch_bounds__(kHeadThreads) number_kernel(const uint32_t* keys, const int64_t* n_dev, Numbering N,
+                                                              const uint32_t* counts, int32_t* err) {
+  __shared__ uint32_t scratch[32];
+  range_sort::wait_previous();
+  const int64_t n = __ldcg(n_dev);
+  const range_sort::Range r = range_sort::range_of(n);
+  uint32_t part = 0, run;
+  for (int b = threadIdx.x; b < int(blockIdx.x); b += kHeadThreads) part += __ldcg(counts + b);
+  block_exclusive_scan<uint32_t>(part, scratch, &run);
+  for (int64_t t0 = 0; t0 < r.count; t0 += kHeadTile) {
+    const int64_t i0 = r.first + t0 + int64_t(threadIdx.x) * kHeadItems, end = r.first + r.count;
+    uint32_t k[kHeadItems], prev = 0;
+    if (i0 < end) {  // (begins at a multiple of 8; the array ends at one of 64)
+      const uint4 a = __ldcg(reinterpret_cast<const uint4*>(keys + i0)), b = __ldcg(reinterpret_cast<const uint4*>(keys + i0) + 1);
+      k[0] = a.x, k[1] = a.y, k[2] = a.z, k[3] = a.w, k[4] = b.x, k[5] = b.y, k[6] = b.z, k[7] = b.w;
+      if (i0 > 0) prev = __ldcg(keys + i0 - 1);
     }
-    return;
-  }
-  const int64_t i0 = tile * kHeadTile + threadIdx.x * kHeadItems;
-  uint32_t k[kHeadItems];
-  uint32_t prev = 0;
+    uint32_t heads = 0, mine = 0;
 #pragma unroll
-  for (int q = 0; q < kHeadItems; ++q) k[q] = i0 + q < n ? keys[i0 + q] : 0u;
-  if (i0 > 0 && i0 < n) prev = keys[i0 - 1];
-  uint32_t heads = 0, mine = 0;
+    for (int q = 0; q < kHeadItems; ++q) {
+      const bool h = i0 + q < end && (i0 + q == 0 || k[q] != (q ? k[q - 1] : prev));
+      heads |= uint32_t(h) << q;
+      mine += h;
+    }
+    uint32_t total;
+    uint32_t u = run + block_exclusive_scan<uint32_t>(mine, scratch, &total);
+    run += total;
 #pragma unroll
-  for (int q = 0; q < kHeadItems; ++q) {
-    const bool h = i0 + q < n && (i0 + q == 0 || k[q] != (q ? k[q - 1] : prev));
-    heads |= uint32_t(h) << q;
-    mine += h;
-  }
-  uint32_t total;
-  const uint32_t in_tile = block_exclusive_scan<uint32_t>(mine, scan, &total);
-  if (threadIdx.x < 32) {
-    const uint64_t e = warp_lookback(status, 1, tile, total, err, limit);
-    if (threadIdx.x == 0) s_excl = e;
-  }
-  __syncthreads();
-  uint64_t u = s_excl + in_tile;
-  if (u + mine > uint64_t(n)) return;  // a wait that gave up left no usable number: write nothing
-#pragma unroll
-  for (int q = 0; q < kHeadItems; ++q) {
-    const int64_t i = i0 + q;
-    if (i < n && (i & ((int64_t(1) << N.chunk_log2) - 1)) == 0) N.before[i >> N.chunk_log2] = uint32_t(u);
-    if ((heads >> q) & 1u) {
-      N.start[u] = uint32_t(i);
-      if (int64_t(u) < N.cap) N.rows[u] = int64_t(k[q]);
-      else set_err(err, FS_ERR_CAPACITY);
-      ++u;
+    for (int q = 0; q < kHeadItems; ++q) {
+      const int64_t i = i0 + q;
+      if (i < end && (i & ((int64_t(1) << N.chunk_log2) - 1)) == 0) N.before[i >> N.chunk_log2] = u;
+      if ((heads >> q) & 1u) {
+        N.start[u] = uint32_t(i);
+        if (int64_t(u) < N.cap) N.rows[u] = int64_t(k[q]);
+        else set_err(err, FS_ERR_CAPACITY);
+        ++u;
+      }
     }
   }
-  if (tile == ntiles - 1 && threadIdx.x == kHeadThreads - 1) {
-    *N.count = int64_t(u);
-    N.start[u] = uint32_t(n);
+  if (threadIdx.x == 0 && (r.count > 0 ? r.first + r.count == n : n == 0 && blockIdx.x == 0)) {
+    *N.count = int64_t(run);
+    N.start[run] = uint32_t(n);
   }
 }
 
@@ -426,23 +417,25 @@ __global__ void __launch_bounds__(kRedThreads, 6) grad_reduce_kernel(
   if (open) partial(from_prev ? part_head : part_tail);  // the row goes on: it began before this tile, or here
 }
 
-// One warp per tile in which a row begins that goes on in the next tile:
-// the row's sum is the tile's tail plus the heads of the following tiles up to
-// the row's last.  Rows over more than kLongTiles tiles are added by the whole
-// block: warp w takes every 32nd tile, then the warps' sums in warp order.
-// VEC columns a lane.
-constexpr int kJoinThreads = 1024, kJoinWarps = kJoinThreads / 32, kLongTiles = 16;
+// The rows that begin in a tile and go on in the next: a row's sum is its tile's
+// tail plus the heads of the following tiles up to the row's last.  A block takes
+// one contiguous range of tiles: a thread per tile finds its row and its last
+// tile (a chain of dependent loads, walked for the whole range together), then
+// a warp per row adds.  Rows over more than kLongTiles tiles are added by the whole
+// block: warp w takes every 16th tile, then the warps' sums in warp order.
+// VEC columns a lane.  (A warp per tile that walked the chain itself took 39 us
+// for 2M entries of 128, this @JOIN@.)
+constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32, kLongTiles = 16, kJoinPerSm = 2;
 
 template <class EO, int VEC>
-__global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const uint32_t* __restrict__ keys,
-                                                                 const int64_t* __restrict__ n_dev,
-                                                                 const uint32_t* __restrict__ start,
-                                                                 const uint32_t* __restrict__ before, int chunk_log2,
-                                                                 int32_t dim, float scale, void* __restrict__ grads,
-                                                                 int64_t cap, const float* __restrict__ part_head,
-                                                                 const float* __restrict__ part_tail) {
-  __shared__ uint32_t long_row[kJoinWarps];
+__global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) grad_join_kernel(
+    const uint32_t* __restrict__ keys, const int64_t* __restrict__ n_dev, const uint32_t* __restrict__ start,
+    const uint32_t* __restrict__ before, int chunk_log2, int32_t dim, float scale, void* __restrict__ grads, int64_t cap,
+    const float* __restrict__ part_head, const float* __restrict__ part_tail) {
+  __shared__ uint32_t row[kJoinThreads];           // rows to join, in tile order
+  __shared__ int32_t from[kJoinThreads], to[kJoinThreads];  // their first and last tiles
   __shared__ float sums[kJoinWarps][32 * VEC];
+  __shared__ uint32_t scratch[32];
   const int64_t n = *n_dev;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t ntiles = (n + (int64_t(1) << chunk_log2) - 1) >> chunk_log2;
@@ -465,56 +458,65 @@ __global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const uint32_t*
       for (int k = 0; k < VEC; ++k) a[k] += x[k];
     }
   };
-  auto last_tile = [&](uint32_t u) {
-    const int64_t v = int64_t(start[u + 1] - 1) >> chunk_log2;
-    return v < ntiles ? v : ntiles - 1;
-  };
   auto put = [&](int64_t u, int c, float (&a)[VEC]) {
 #pragma unroll
     for (int k = 0; k < VEC; ++k) a[k] *= scale;
     store_vec<EO, VEC, false>(grads, u * dim + c, a);
   };
-  for (int64_t t0 = int64_t(blockIdx.x) * kJoinWarps; t0 < ntiles; t0 += int64_t(gridDim.x) * kJoinWarps) {
-    const int64_t t = t0 + warp;
-    bool is_long = false;
-    const int64_t edge = (t + 1) << chunk_log2;
-    if (edge < n && keys[edge - 1] == keys[edge]) {
-      const uint32_t u = before[t + 1] - 1;
-      // (u < n unless the numbering gave up; it begins in this tile)
-      if (int64_t(u) < n && int64_t(u) < cap && int64_t(start[u]) >= (t << chunk_log2)) {
-        const int64_t last = last_tile(u);
-        is_long = last - t > kLongTiles;
-        if (!is_long)
-          for (int c = lane * VEC; c < dim; c += 32 * VEC) {
-            float a[VEC];
-            load_vec<F32, VEC, true>(part_tail, t * dim + c, a);
-            sum_tiles(a, t + 1, last, 1, c);
-            put(u, c, a);
-          }
+  const int64_t per = (ntiles + gridDim.x - 1) / gridDim.x;
+  const int64_t begin = per * blockIdx.x, end = begin + per < ntiles ? begin + per : ntiles;
+  for (int64_t t0 = begin; t0 < end; t0 += kJoinThreads) {
+    const int64_t t = t0 + threadIdx.x, edge = (t + 1) << chunk_log2;
+    uint32_t u = 0;
+    int64_t last = 0;
+    bool joins = false;
+    if (t < end && edge < n) {
+      const uint32_t k0 = keys[edge - 1], k1 = keys[edge], after = before[t + 1];  // (one latency for the three)
+      if (k0 == k1) {
+        u = after - 1;
+        if (int64_t(u) < cap) {
+          const uint32_t s = start[u], e = start[u + 1];
+          joins = int64_t(s) >= (t << chunk_log2);  // it begins in this tile
+          last = int64_t(e - 1) >> chunk_log2;
+        }
       }
     }
-    if (lane == 0) long_row[warp] = is_long ? 1u : 0u;
+    uint32_t rows;
+    const uint32_t at = block_exclusive_scan<uint32_t>(joins ? 1u : 0u, scratch, &rows);
+    if (joins) {
+      row[at] = u;
+      from[at] = int32_t(t);
+      to[at] = int32_t(last);
+    }
     __syncthreads();
-    for (int w = 0; w < kJoinWarps; ++w) {
-      if (!long_row[w]) continue;  // (the same for every thread)
-      const int64_t tl = t0 + w;
-      const uint32_t u = before[tl + 1] - 1;
-      const int64_t last = last_tile(u);
+    for (uint32_t i = warp; i < rows; i += kJoinWarps) {
+      const int64_t tt = from[i], last_t = to[i];
+      if (last_t - tt > kLongTiles) continue;
+      for (int c = lane * VEC; c < dim; c += 32 * VEC) {
+        float a[VEC];
+        load_vec<F32, VEC, true>(part_tail, tt * dim + c, a);
+        sum_tiles(a, tt + 1, last_t, 1, c);
+        put(row[i], c, a);
+      }
+    }
+    for (uint32_t i = 0; i < rows; ++i) {
+      const int64_t tt = from[i], last_t = to[i];
+      if (last_t - tt <= kLongTiles) continue;  // (the same for every thread)
       for (int c0 = 0; c0 < dim; c0 += 32 * VEC) {
         const int c = c0 + lane * VEC;
         float a[VEC];
 #pragma unroll
         for (int k = 0; k < VEC; ++k) a[k] = 0.f;
-        if (c < dim) sum_tiles(a, tl + 1 + warp, last, kJoinWarps, c);
+        if (c < dim) sum_tiles(a, tt + 1 + warp, last_t, kJoinWarps, c);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) sums[warp][lane * VEC + k] = a[k];
         __syncthreads();
         if (warp == 0 && c < dim) {
-          load_vec<F32, VEC, true>(part_tail, tl * dim + c, a);
+          load_vec<F32, VEC, true>(part_tail, tt * dim + c, a);
           for (int q = 0; q < kJoinWarps; ++q)
 #pragma unroll
             for (int k = 0; k < VEC; ++k) a[k] += sums[q][lane * VEC + k];
-          put(u, c, a);
+          put(row[i], c, a);
         }
         __syncthreads();
       }
@@ -536,34 +538,32 @@ int chunk_log2_for(int64_t T) {
 }
 
 struct GradLayout {
-  radix::SortPlan plan;
   int chunk_log2 = 3;
-  int64_t tiles = 0, head_tiles = 0;
+  int64_t tiles = 0;
 };
 
-GradLayout grad_layout(int64_t T, int64_t R) {
+GradLayout grad_layout(int64_t T) {
   GradLayout L;
-  L.plan = radix::SortPlan(T, radix::bits_for(uint64_t(R - 1)));
   L.chunk_log2 = chunk_log2_for(T);
   L.tiles = (T + (int64_t(1) << L.chunk_log2) - 1) >> L.chunk_log2;
-  L.head_tiles = (T + kHeadTile - 1) / kHeadTile;
   return L;
 }
 
 struct GradWs {
-  radix::SortWs W;
+  range_sort::Ws sort;
   uint32_t *start = nullptr, *before = nullptr;
+  uint32_t* heads = nullptr;  // distinct rows that begin in each block's range
   float *part_head = nullptr, *part_tail = nullptr;
-  uint64_t* status = nullptr;  // look-back words of the heads' tiles, then the ticket
 };
 
-template <class Ws>
-void take_grad(const GradLayout& L, int64_t T, int32_t dim, Ws& ws, GradWs& G) {
+template <class Cursor>
+void take_grad(const GradLayout& L, int64_t T, int32_t dim, Cursor& ws, GradWs& G) {
+  range_sort::take(T, ws, G.sort);
   G.start = ws.template take<uint32_t>(size_t(T) + 1);
   G.before = ws.template take<uint32_t>(size_t(L.tiles) + 1);
+  G.heads = ws.template take<uint32_t>(range_sort::kMaxBlocks);
   G.part_head = ws.template take<float>(size_t(L.tiles) * dim);
   G.part_tail = ws.template take<float>(size_t(L.tiles) * dim);
-  G.status = ws.template take<uint64_t>(size_t(L.head_tiles) + 1);
 }
 
 template <class EI, class EO, int VEC, int LPR>
@@ -571,7 +571,7 @@ void launch_reduce_lpr(const GradLayout& L, const GradWs& G, const uint32_t* sk,
                        int32_t dim, float scale, void* grads, int64_t cap, cudaStream_t st) {
   const int64_t threads = L.tiles * LPR;
   const dim3 grid(unsigned((threads + kRedThreads - 1) / kRedThreads), unsigned((dim + LPR * VEC - 1) / (LPR * VEC)));
-  grad_reduce_kernel<EI, EO, VEC, LPR><<<grid, kRedThreads, 0, st>>>(sk, sv, G.W.pass.n_valid, G.before, L.chunk_log2,
+  grad_reduce_kernel<EI, EO, VEC, LPR><<<grid, kRedThreads, 0, st>>>(sk, sv, G.sort.n, G.before, L.chunk_log2,
                                                                      dout, dim, scale, grads, cap, G.part_head,
                                                                      G.part_tail);
 }
@@ -613,7 +613,7 @@ bool launch_small_sort(const int64_t* ids, int64_t T, int64_t R, uint32_t* sv, c
       return false;
     ready.fetch_or(bit);
   }
-  const int kb = radix::bits_for(uint64_t(R));  // room for a key past every row
+  const int kb = range_sort::bits_for(uint64_t(R));  // room for a key past every row
   small_sort_kernel<ITEMS><<<1, kSmallThreads, small_smem<ITEMS>(), st>>>(ids, int32_t(T), R, kb, sv, N, err);
   return true;
 }
@@ -634,11 +634,11 @@ using namespace fs;
 
 extern "C" size_t fs_emb_grad_rows_workspace_size(int64_t T, int64_t num_rows, int32_t dim) {
   if (T < 0 || T > INT32_MAX || num_rows < 1 || num_rows >= (int64_t(1) << 32) || dim < 1) return 0;
-  const GradLayout L = grad_layout(T, num_rows);
+  const GradLayout L = grad_layout(T);
   WsCounter c;
   GradWs G;
   take_grad(L, T, dim, c, G);
-  return c.used + L.plan.bytes() + 256;
+  return c.used + 256;
 }
 
 extern "C" fs_status fs_emb_grad_rows(int64_t num_rows, int32_t dim, const int64_t* ids, int64_t T, const void* dout,
@@ -659,15 +659,14 @@ extern "C" fs_status fs_emb_grad_rows(int64_t num_rows, int32_t dim, const int64
   if (!aligned(ids, 8) || !aligned(rows, 8) || !aligned(dout, ib) || !aligned(row_grads, ob)) return FS_ERR_ALIGNMENT;
   if (!ws || ws_bytes < fs_emb_grad_rows_workspace_size(T, num_rows, dim)) return FS_ERR_WORKSPACE;
 
-  const GradLayout L = grad_layout(T, num_rows);
+  const GradLayout L = grad_layout(T);
   WsCursor cur(ws, ws_bytes);
   GradWs G;
-  if (!radix::carve_sort_ws(L.plan, cur, G.W)) return FS_ERR_WORKSPACE;
   take_grad(L, T, dim, cur, G);
   if (!cur.ok) return FS_ERR_WORKSPACE;
   const Numbering N{rows, cap_rows, count, G.start, G.before, L.chunk_log2};
   int launches = 0;
-  uint32_t *sk = G.W.k[0], *sv = G.W.v[0];
+  uint32_t *sk = G.sort.k[0], *sv = G.sort.v[0];
   const bool small = T <= kSmallMax;
   if (small) {
     bool ok;
@@ -680,13 +679,17 @@ extern "C" fs_status fs_emb_grad_rows(int64_t num_rows, int32_t dim, const int64
     if (!ok) return FS_ERR_CUDA;
     launches += 1;
   } else {
-    const fs_status s = radix::run_sort(SrcIds{ids, num_rows}, L.plan, G.W, err, st, &sk, &sv, &launches);
+    int side = 0;
+    const fs_status s = range_sort::sort(ids, T, num_rows, range_sort::bits_for(uint64_t(num_rows - 1)), G.sort, err, st, &side,
+                                         &launches);
     if (s != FS_OK) return s;
-    if (cudaMemsetAsync(G.status, 0, (size_t(L.head_tiles) + 1) * sizeof(uint64_t), st) != cudaSuccess)
+    sk = G.sort.k[side];
+    sv = G.sort.v[side];
+    const int blocks = range_sort::blocks_for(T);
+    if (range_sort::launch_after(head_count_kernel, blocks, kHeadThreads, st, sk, G.sort.n, G.heads) != cudaSuccess ||
+        range_sort::launch_after(number_kernel, blocks, kHeadThreads, st, sk, G.sort.n, N, G.heads, err) != cudaSuccess)
       return FS_ERR_CUDA;
-    heads_kernel<<<unsigned(L.head_tiles), kHeadThreads, 0, st>>>(
-        sk, G.W.pass.n_valid, N, G.status, reinterpret_cast<uint32_t*>(G.status + L.head_tiles), err, spin_limit());
-    launches += 1;
+    launches += 2;
   }
   const int vec = ib == 4 ? 4 : 8;
   // 16-byte loads of dout where rows and addresses allow them, element by element otherwise
@@ -708,9 +711,9 @@ extern "C" fs_status fs_emb_grad_rows(int64_t num_rows, int32_t dim, const int64
     count_launch(launches + 1);
     return launch_status();
   }
-  const int64_t want = (L.tiles + kJoinWarps - 1) / kJoinWarps, most = int64_t(sm_count()) * 8;
+  const int64_t want = (L.tiles + kJoinWarps - 1) / kJoinWarps, most = int64_t(sm_count()) * kJoinPerSm;
   auto join = [&](auto kern) {
-    kern<<<unsigned(want < most ? want : most), kJoinThreads, 0, st>>>(sk, G.W.pass.n_valid, G.start, G.before,
+    kern<<<unsigned(want < most ? want : most), kJoinThreads, 0, st>>>(sk, G.sort.n, G.start, G.before,
                                                                        L.chunk_log2, dim, scale, row_grads, cap_rows,
                                                                        G.part_head, G.part_tail);
   };
