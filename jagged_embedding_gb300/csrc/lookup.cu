@@ -17,7 +17,8 @@ constexpr int kLookupThreads = 256;
 // loaded before this iteration's rows.  Rows of more than LPR * VEC elements
 // take several steps.
 // Bound by HBM: 8 B of ID, one table row (distinct rows once, the others from
-// L2) and one output row per position.
+// L2) and one output row per position.  2M Zipf IDs over 10M rows of 128 bf16:
+// 119 us, 5.7 TB/s of those bytes.  257 IDs: 3 us, two dependent reads.
 template <class EI, class EO, int VEC, int LPR>
 __global__ void __launch_bounds__(kLookupThreads, 3) lookup_kernel(const void* __restrict__ table, int64_t R, int32_t dim,
                                                                    const int64_t* __restrict__ ids, int64_t T,

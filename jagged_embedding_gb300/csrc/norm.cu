@@ -10,6 +10,8 @@
 //
 // Both passes are bound by HBM: every input is read once and every output
 // written once, a row staying in the registers of the G threads that own it.
+// 400,000 rows of 512 bf16: forward with residual and 8-bit output 227 us, 6.3 TB/s;
+// backward 272 us, 6.0 TB/s.  A few hundred rows take 3 and 4.5 us.
 #include <cooperative_groups.h>
 
 #include <type_traits>

@@ -17,7 +17,10 @@
 // the same bits from run to run.
 //
 // Bound by HBM: 8 B of ID and one row of dout per position, one row of G per
-// distinct ID; the sort moves about 20 B per ID and pass beside that.
+// distinct ID; the sort moves about 20 B per ID and pass beside that.  2M Zipf IDs
+// over 10M rows, bf16 rows of 128 into fp32 rows: 252 us a call -- sort 77, numbering
+// 19, reduce 138 (0.79 GB, 5.7 TB/s), join 14 -- of which those bytes alone would take 124.
+// 2000 IDs: 17 us, half of it the one block that sorts.
 #include <atomic>
 
 #include "convert.cuh"
@@ -424,7 +427,7 @@ __global__ void __launch_bounds__(kRedThreads, 6) grad_reduce_kernel(
 // a warp per row adds.  Rows over more than kLongTiles tiles are added by the whole
 // block: warp w takes every 16th tile, then the warps' sums in warp order.
 // VEC columns a lane.  (A warp per tile that walked the chain itself took 39 us
-// for 2M entries of 128, this @JOIN@.)
+// for 2M entries of 128, this 18.)
 constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32, kLongTiles = 16, kJoinPerSm = 2;
 
 template <class EO, int VEC>
@@ -528,9 +531,9 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) grad_join_kernel(
 // ------------------------------------------------------------- host side
 
 // Entries per reduce tile: 8 for the smallest batches (one step of loads),
-// doubled while more than 8192 tiles remain, at most 64 (2M entries of 128 bf16: 306 us a pass with 64 and with 128
-// 316, 32 324): enough groups of lanes to
-// fill the GPU, few edges (each costs a partial row written and read).
+// doubled while more than 8192 tiles remain, at most 64: enough groups of lanes to
+// fill the GPU, few edges, each of which costs a partial row written and read
+// (2M entries of 128 bf16: 64 was 10 us a call faster than 128 and 18 than 32).
 int chunk_log2_for(int64_t T) {
   int c = 3;
   while (c < 6 && (T >> c) > 8192) ++c;

@@ -154,6 +154,29 @@ def test_row_grads_hot_rows_are_the_same_run_to_run():
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T,R,hot", [(9_000, 200, 1), (700_001, 1 << 16, 3), (2_600_003, (1 << 24) + 1, 1_000),
+                                     (5_000_003, (1 << 32) - 1, 7)])
+def test_row_grads_of_whole_numbers_are_exact(T, R, hot):
+    """One to four sorting passes, ranges of several tiles, rows over thousands of tiles, IDs out of range among
+    them: sums of small whole numbers are exact in 32 bits, in any order."""
+    D = 4
+    g = torch.Generator(device=DEV).manual_seed(T)
+    ids = torch.randint(0, R, (T,), generator=g, device=DEV)
+    ids = torch.where(torch.rand(T, generator=g, device=DEV) < 0.5, ids % hot * (R // hot), ids)
+    ids[torch.rand(T, generator=g, device=DEV) < 0.01] = R
+    dout = torch.randint(-2, 3, (T, D), generator=g, device=DEV).to(BF16)
+    rows, grads, count, err = B.fs_emb_grad_rows(ids, dout, R, 2.0)
+    with pytest.raises(B.FsError) as e:
+        B.check(err)
+    assert e.value.code == 2
+    keep = ids < R
+    uniq, inv = torch.unique(ids[keep], return_inverse=True)
+    ref = torch.zeros(uniq.numel(), D, dtype=torch.float64).index_add_(0, inv.cpu(), dout[keep].double().cpu())
+    n = uniq.numel()
+    assert int(count) == n and torch.equal(rows[:n], uniq)
+    assert torch.equal(grads[:n].double().cpu(), ref * 2.0)
+
+
 def test_row_grads_equal_differences():
     """The gradient of sum(dout * lookup(W)) in W, by central differences along random directions (64 bits)."""
     T, R, D, scale = 500, 40, 16, 3.0
