@@ -446,10 +446,10 @@ struct Taker {
   }
 };
 
-// The products are issued by one thread in batches: what one batch waits for and
-// the descriptors of its operands are found before, by the whole warp, so that between two products
+// The products are issued by one warp in batches: what one batch waits for and
+// the descriptors of its operands are found before, so that between two products
 // of a batch there is nothing but the products (a few dozen instructions of one warp
-// beside sixteen busy ones take longer than the queue of products lasts).
+// beside busy ones take longer than the queue of products lasts).
 
 // D[128 x 128] = A B^T over DH columns, both tiles K-major: descriptors of tc::desc_k.
 template <int DH>
@@ -474,21 +474,14 @@ __device__ __forceinline__ void mma_cols(uint32_t d, uint32_t a0, uint32_t a1, u
     tc::mma_ts<false>(d, (k < 4 ? a0 + 8 * k : a1 + 8 * (k - 4)), tc::at(b, k * 2048), id, true);
 }
 
-// The same from shared-memory addresses, called by a whole warp.
+// The same from shared-memory addresses.
 template <int DH>
-__device__ __forceinline__ void warp_mma_rows(uint32_t d, uint32_t a, uint32_t b) {
-  const uint32_t da = tc::desc_k(a), db = tc::desc_k(tc::uni(b));
-  if ((threadIdx.x & 31) == 0) mma_rows<DH>(d, da, db);
+__device__ __forceinline__ void mma_rows_at(uint32_t d, uint32_t a, uint32_t b) {
+  mma_rows<DH>(d, tc::desc_k(a), tc::desc_k(tc::uni(b)));
 }
 template <int DH>
-__device__ __forceinline__ void warp_mma_cols(uint32_t d, uint32_t a0, uint32_t a1, uint32_t b, bool acc) {
-  const uint32_t db = tc::desc_mn(tc::uni(b), kBox);
-  if ((threadIdx.x & 31) == 0) mma_cols<DH>(d, a0, a1, db, acc);
-}
-
-// Commit by the issuing lane of a whole warp.
-__device__ __forceinline__ void commit(uint32_t bar) {
-  if ((threadIdx.x & 31) == 0) tc::commit(bar);
+__device__ __forceinline__ void mma_cols_at(uint32_t d, uint32_t a0, uint32_t a1, uint32_t b, bool acc) {
+  mma_cols<DH>(d, a0, a1, tc::desc_mn(tc::uni(b), kBox), acc);
 }
 
 // 32 fp32 columns of each lane's row, scaled, as bf16: `to` is column 0 of the
@@ -703,28 +696,28 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
               if (!(ok = wait(p_ready + 8 * i, done[i], a))) break;
               ++done[i];
               tc::fence_after();
-              warp_mma_cols<DH>(o_at + DH * i, s_at + 128 * i, s_at + 128 * i + 32, kv_at + v.s * TB, acc[i]);
+              mma_cols_at<DH>(o_at + DH * i, s_at + 128 * i, s_at + 128 * i + 32, kv_at + v.s * TB, acc[i]);
               acc[i] = true;
             }
             if (j < f.n && f.meets(i, j)) {
               // x overwrites p: the products execute in the order they are issued
-              warp_mma_rows<DH>(s_at + 128 * i, q_at + i * TB, kv_at + key.s * TB);
-              commit(s_full + 8 * i);
+              mma_rows_at<DH>(s_at + 128 * i, q_at + i * TB, kv_at + key.s * TB);
+              tc::commit(s_full + 8 * i);
             }
           }
           if (!ok) break;
-          if (j > 0) commit(free + 8 * v.s);
-          if (j < f.n) commit(free + 8 * key.s);
-          if (j == f.n - 1) commit(q_free);
+          if (j > 0) tc::commit(free + 8 * v.s);
+          if (j < f.n) tc::commit(free + 8 * key.s);
+          if (j == f.n - 1) tc::commit(q_free);
           if (j == f.n) {  // (a barrier for each: a warpgroup without work would fall phases behind one of both)
-            commit(o_full);
-            if (f.both) commit(o_full + 8);
+            tc::commit(o_full);
+            if (f.both) tc::commit(o_full + 8);
           }
         }
         ks.back(2);  // (the last step has no key tile)
       }
       if (!ok) {
-        commit(drain);
+        tc::commit(drain);
         wait(drain, 0, a);
       }
     }
@@ -961,12 +954,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
     auto scores = [&]() {           // x of the next key tile, into columns that the last tile's readers have left
       const uint32_t k_desc = tc::uni(tc::desc_k(kv_at + ks.s * TB));
       if (!wait(full + 8 * ks.s, ks.phase, a) || (c > 0 && !wait(s_read, c - 1, a))) return false;
-      if (lane == 0) {
-        tc::fence_after();
-        mma_rows<DH>(s_at, q_desc, k_desc);
-        tc::commit(s_full);
-      }
-      __syncwarp();
+      tc::fence_after();
+      mma_rows<DH>(s_at, q_desc, k_desc);
+      tc::commit(s_full);
       ks.skip(2);
       return true;
     };
@@ -977,21 +967,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
       const uint32_t k_free = tc::uni(free + 8 * kq.s), v_free = tc::uni(free + 8 * vs.s);
       if (more && !wait(full + 8 * vs.s, vs.phase, a)) return false;
       if (sum && !wait(ds_ready, c - 1, a)) return false;
-      if (lane == 0) {
-        tc::fence_after();
-        if (sum) {
-          mma_cols<DH>(dq_at, dp_at, dp_at + 64, kq_desc, acc);
-          tc::commit(k_free);
-        }
-        if (more) {
-          mma_rows<DH>(dp_at, do_desc, v_desc);
-          tc::commit(dp_full);
-          tc::commit(v_free);
-        } else {
-          tc::commit(dq_full);
-        }
+      tc::fence_after();
+      if (sum) {
+        mma_cols<DH>(dq_at, dp_at, dp_at + 64, kq_desc, acc);
+        tc::commit(k_free);
       }
-      __syncwarp();
+      if (more) {
+        mma_rows<DH>(dp_at, do_desc, v_desc);
+        tc::commit(dp_full);
+        tc::commit(v_free);
+      } else {
+        tc::commit(dq_full);
+      }
       if (sum) kq.skip(2);
       if (more) vs.skip(2);
       return true;
@@ -1004,13 +991,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
       if (!(ok = scores() && sums_and_products(false, false, true))) break;
       for (int j = 0; j < n; ++j) {
         ++c;
-        if (j + 1 == n) commit(q_free);
+        if (j + 1 == n) tc::commit(q_free);
         else if (!(ok = scores())) break;
         if (!(ok = sums_and_products(true, j != 0, j + 1 < n))) break;
       }
     }
     if (!ok) {
-      commit(drain);
+      tc::commit(drain);
       wait(drain, 0, a);
     }
   } else {
@@ -1273,38 +1260,32 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
           const uint32_t do_free = tc::uni(free + 8 * dv.s);
           if (more && !(ok = wait(full + 8 * qs.s, qs.phase, a))) break;
           if (sum && !(ok = wait(p_ready, c, a))) break;
-          if (lane == 0) {
-            tc::fence_after();
-            if (sum) {
-              mma_cols<DH>(dv_at, s_at, s_at + 64, do_desc, j != 0);
-              tc::commit(do_free);
-            }
-            if (more) {
-              mma_rows<DH>(s_at, k_desc, q_desc);
-              tc::commit(s_full);
-            }
+          tc::fence_after();
+          if (sum) {
+            mma_cols<DH>(dv_at, s_at, s_at + 64, do_desc, j != 0);
+            tc::commit(do_free);
           }
-          __syncwarp();
+          if (more) {
+            mma_rows<DH>(s_at, k_desc, q_desc);
+            tc::commit(s_full);
+          }
         }
         const uint32_t q_desc = tc::uni(tc::desc_mn(qd_at + qk.s * TB, kBox)), do_desc = tc::uni(tc::desc_k(qd_at + ds.s * TB));
         const uint32_t q_free = tc::uni(free + 8 * qk.s);
         if (more && !(ok = wait(full + 8 * ds.s, ds.phase, a))) break;
         if (sum && !(ok = wait(ds_ready, c, a))) break;
-        if (lane == 0) {
-          tc::fence_after();
-          if (sum) {
-            mma_cols<DH>(dk_at, dp_at, dp_at + 64, q_desc, j != 0);
-            tc::commit(q_free);
-          }
-          if (more) {
-            mma_rows<DH>(dp_at, v_desc, do_desc);
-            tc::commit(dp_full);
-            if (j + 2 == n) tc::commit(kv_free);
-          } else {
-            tc::commit(sums_full);
-          }
+        tc::fence_after();
+        if (sum) {
+          mma_cols<DH>(dk_at, dp_at, dp_at + 64, q_desc, j != 0);
+          tc::commit(q_free);
         }
-        __syncwarp();
+        if (more) {
+          mma_rows<DH>(dp_at, v_desc, do_desc);
+          tc::commit(dp_full);
+          if (j + 2 == n) tc::commit(kv_free);
+        } else {
+          tc::commit(sums_full);
+        }
         if (sum) {
           dv.skip(2), qk.skip(2);
           ++c;
@@ -1313,7 +1294,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
       }
     }
     if (!ok) {
-      commit(drain);
+      tc::commit(drain);
       wait(drain, 0, a);
     }
   } else {

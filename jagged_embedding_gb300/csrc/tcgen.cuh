@@ -104,21 +104,27 @@ __device__ __forceinline__ void st32(uint32_t addr, const uint32_t* u) {
       : "memory");
 }
 
-// ------------------------------------------------------------- MMA (one thread)
+// ------------------------------------------------------------- MMA
+//
+// Called by a whole converged warp; one elected lane, always the same, issues.  The election
+// stands in front of every instruction, not around them in a branch: outside of divergent code the operands
+// stay in uniform registers from one product to the next (8 products of 128 x 128 x 16 issued
+// in 148 cycles; behind a branch on the lane 400, hardly less than the 512 they run, so that
+// whatever else the scheduler ran in between was lost to the tensor cores).
 
 // D (tensor memory, fp32) = A * B + (acc ? D : 0), both operands in shared memory.
 template <bool FIRST>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
   if constexpr (FIRST)
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
         "l"(a), "l"(b), "r"(id), "r"(uint32_t(acc))
         : "memory");
   else
     asm volatile(
-        "{\n .reg .pred p;\n setp.eq.u32 p, 0, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "{\n .reg .pred p, e;\n setp.eq.u32 p, 0, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
         "l"(a), "l"(b), "r"(id)
         : "memory");
 }
@@ -128,21 +134,24 @@ template <bool FIRST>
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool acc) {
   if constexpr (FIRST)
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
         "r"(a), "l"(b), "r"(id), "r"(uint32_t(acc))
         : "memory");
   else
     asm volatile(
-        "{\n .reg .pred p;\n setp.eq.u32 p, 0, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "{\n .reg .pred p, e;\n setp.eq.u32 p, 0, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
         "r"(a), "l"(b), "r"(id)
         : "memory");
 }
 
-// One arrival on `bar` once every tcgen05 operation this thread issued before has completed.
+// One arrival on `bar` once every tcgen05 operation the elected lane issued before has completed.
 __device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar)
+      : "memory");
 }
 
 // ------------------------------------------------------------- barriers and TMA
