@@ -851,8 +851,9 @@ __device__ __forceinline__ Tile uniform_tile(Tile x) {
 
 // dq of one query tile and head a unit.  A thread holds one query row and 64 of
 // the 128 keys.  Per key tile: x = q k^T and do v^T into 128 columns each; p = exp(x - lse)
-// stays in registers and frees x, so the next tile's x is computed while
-// ds = p * (do v^T - delta) is formed; ds (bf16) goes over do v^T and multiplies k.
+// stays in registers and frees x; ds = p * (do v^T - delta), in bf16, goes over do v^T and
+// multiplies k.  do v^T has two places that take turns, so the next tile's x and do v^T are computed while
+// ds is formed (with one place they waited for the product of ds: 323 us a backward pass instead of 314).
 // delta = dout.out: the unit's rows of out come through the ring in front of its
 // keys.  Where there is one key tile delta = sum p * (do v^T) is at hand instead, free of the rounding
 // of out, which matters most there: few keys leave out about as large as v (8 samples of up to
@@ -885,19 +886,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                                                                  const __grid_constant__ CUtensorMap mdo, AttnArgs a) {
   constexpr int TB = tile_bytes<DH>(), NS = bwd_slots<DH>();
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ __align__(8) uint64_t bars[13 + 2 * NS];
+  __shared__ __align__(8) uint64_t bars[15 + 2 * NS];
   __shared__ uint32_t tmem_at;
   __shared__ DqUnit given[4];
   __shared__ float half_delta[2][kTile];
   const uint32_t q_at = bulk::smem_addr(smem), do_at = q_at + TB, kv_at = do_at + TB;
   const uint32_t bar = bulk::smem_addr(bars);
-  const uint32_t q_full = bar, q_free = bar + 8, s_full = bar + 16, dp_full = bar + 24, s_read = bar + 32,
-                 ds_ready = bar + 40, delta_in = bar + 48, dq_full = bar + 56, tail = bar + 64, drain = bar + 96,
-                 full = bar + 104, free = full + 8 * NS;
+  const uint32_t q_full = bar, q_free = bar + 8, s_full = bar + 16, dp_full = bar + 24, s_read = bar + 40,
+                 ds_ready = bar + 48, delta_in = bar + 64, dq_full = bar + 72, tail = bar + 80, drain = bar + 112,
+                 full = bar + 120, free = full + 8 * NS;  // (dp_full, ds_ready: one for each place)
   const int warp = int(tc::uni(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (warp == 8) {
     if (lane == 0) {
-      for (int i = 0; i < 13 + 2 * NS; ++i) bulk::mbar_init(bar + 8 * i, i == 1 ? 9 : (i >= 4 && i <= 6 ? 8 : 1));
+      for (int i = 0; i < 15 + 2 * NS; ++i) bulk::mbar_init(bar + 8 * i, i == 1 ? 9 : (i >= 5 && i <= 8 ? 8 : 1));
       bulk::fence_init();
     }
     __syncwarp();
@@ -910,7 +911,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
   tc::fence_after();
   wait_for_launch();
   let_next_launch();
-  const uint32_t s_at = tc::uni(tmem_at), dp_at = s_at + 128, dq_at = s_at + 256;
+  const uint32_t s_at = tc::uni(tmem_at), dq_at = s_at + 256;
+  auto dp_at = [&](uint32_t tile) { return s_at + 128 + 256 * (tile & 1); };
 
   if (warp == 9) {
     Feeder<DH, NS> feed(smem + 2 * TB, full, free, tail, a);
@@ -949,9 +951,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
   } else if (warp == 8) {
     Place<NS> ks(0), vs(1), kq(0);  // next key and value tile to read, and the key tile of the next dq product
     const uint32_t q_desc = tc::desc_k(q_at), do_desc = tc::desc_k(do_at);
-    uint32_t c = 0;                 // key tiles so far
+    uint32_t c = 0, sums = 0;       // key tiles so far: do v^T issued, and dq products
     bool ok = true;
-    auto scores = [&]() {           // x of the next key tile, into columns that the last tile's readers have left
+    auto scores = [&]() {  // x of the next key tile, into columns that the last tile's readers have left
       const uint32_t k_desc = tc::uni(tc::desc_k(kv_at + ks.s * TB));
       if (!wait(full + 8 * ks.s, ks.phase, a) || (c > 0 && !wait(s_read, c - 1, a))) return false;
       tc::fence_after();
@@ -960,27 +962,28 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
       ks.skip(2);
       return true;
     };
-    // dq of the last ds (where `sum`), then do v^T of the next value tile over it (where `more`): the products
-    // execute in the order they are issued
-    auto sums_and_products = [&](bool sum, bool acc, bool more) {
-      const uint32_t kq_desc = tc::uni(tc::desc_mn(kv_at + kq.s * TB, kBox)), v_desc = tc::uni(tc::desc_k(kv_at + vs.s * TB));
-      const uint32_t k_free = tc::uni(free + 8 * kq.s), v_free = tc::uni(free + 8 * vs.s);
-      if (more && !wait(full + 8 * vs.s, vs.phase, a)) return false;
-      if (sum && !wait(ds_ready, c - 1, a)) return false;
+    auto products = [&]() {  // its do v^T, over the ds of the last tile but one: the products execute in the order they are issued
+      const uint32_t v_desc = tc::uni(tc::desc_k(kv_at + vs.s * TB));
+      const uint32_t v_free = tc::uni(free + 8 * vs.s), dp = tc::uni(dp_at(c)), dp_bar = tc::uni(dp_full + 8 * (c & 1));
+      if (!wait(full + 8 * vs.s, vs.phase, a)) return false;
       tc::fence_after();
-      if (sum) {
-        mma_cols<DH>(dq_at, dp_at, dp_at + 64, kq_desc, acc);
-        tc::commit(k_free);
-      }
-      if (more) {
-        mma_rows<DH>(dp_at, do_desc, v_desc);
-        tc::commit(dp_full);
-        tc::commit(v_free);
-      } else {
-        tc::commit(dq_full);
-      }
-      if (sum) kq.skip(2);
-      if (more) vs.skip(2);
+      mma_rows<DH>(dp, do_desc, v_desc);
+      tc::commit(dp_bar);
+      tc::commit(v_free);
+      vs.skip(2);
+      ++c;
+      return true;
+    };
+    auto sum = [&](bool acc, bool last) {
+      const uint32_t kq_desc = tc::uni(tc::desc_mn(kv_at + kq.s * TB, kBox)), k_free = tc::uni(free + 8 * kq.s);
+      const uint32_t dp = tc::uni(dp_at(sums));
+      if (!wait(ds_ready + 8 * (sums & 1), sums >> 1, a)) return false;
+      tc::fence_after();
+      mma_cols<DH>(dq_at, dp, dp + 64, kq_desc, acc);
+      tc::commit(k_free);
+      if (last) tc::commit(dq_full);
+      kq.skip(2);
+      ++sums;
       return true;
     };
     for (int k = 0; ok; ++k) {
@@ -988,12 +991,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
       const int n = int(tc::uni(uint32_t(given[k & 3].n)));
       if (n < 0) break;
       if (n > 1) ks.skip(1), vs.skip(1), kq.skip(1);  // (the tile of out)
-      if (!(ok = scores() && sums_and_products(false, false, true))) break;
+      if (!(ok = scores() && products())) break;
       for (int j = 0; j < n; ++j) {
-        ++c;
-        if (j + 1 == n) tc::commit(q_free);
+        const bool more = j + 1 < n;
+        // a value tile that is there goes first, one still under way does not hold up dq
+        bool here = false;
+        if (!more) tc::commit(q_free);
         else if (!(ok = scores())) break;
-        if (!(ok = sums_and_products(true, j != 0, j + 1 < n))) break;
+        else if ((here = __all_sync(0xffffffffu, tc::test(full + 8 * vs.s, vs.phase & 1u))) && !(ok = products())) break;
+        if (!(ok = sum(j != 0, !more) && (!more || here || products()))) break;
       }
     }
     if (!ok) {
@@ -1073,14 +1079,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
           p[i] = tc::ex2(p[i]);
           p[i + 1] = tc::ex2(p[i + 1]);
         }
-        if (!(ok = wait(dp_full, seen, a))) break;
+        if (!(ok = wait(dp_full + 8 * (seen & 1), seen >> 1, a))) break;
         tc::fence_after();
+        const uint32_t dp = dp_at(seen) + lanes + cols;
         if (f.n == 1) {
           float d = 0.f;
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             float g[32];
-            tc::ld32(dp_at + lanes + cols + 32 * b, g);
+            tc::ld32(dp + 32 * b, g);
             tc::wait_ld();
             tc::tie32(g);
 #pragma unroll
@@ -1093,7 +1100,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           float g[32];
-          tc::ld32(dp_at + lanes + cols + 32 * b, g);
+          tc::ld32(dp + 32 * b, g);
           tc::wait_ld();
           tc::tie32(g);
 #pragma unroll
@@ -1108,11 +1115,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
 #pragma unroll
           for (int i = 0; i < 32; i += 2) w[16 * b + i / 2] = tc::pack2(g[i], g[i + 1]);
         }
-        tc::st32(dp_at + lanes + cols, w);
+        tc::st32(dp, w);
         tc::wait_st();
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::arrive(ds_ready);
+        if (lane == 0) tc::arrive(ds_ready + 8 * (seen & 1));
       }
       if (!ok || !(ok = wait(dq_full, k, a))) break;
       tc::fence_after();
