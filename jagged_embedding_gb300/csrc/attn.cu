@@ -29,8 +29,8 @@
 // Bound on long samples by the tensor cores and the hand-overs between products
 // and elementwise warps, on short ones by the chain of latencies inside one unit.
 // 22,000 positions of causal samples up to 4096, 8 query and 2 key/value heads of 128:
-// forward 99 us (999 TFLOP/s over visible pairs, tensor pipe 50% active), backward
-// 313 us (789 TFLOP/s over 5 products, 51 and 55% active over the 7 that run).
+// forward 91 us (1090 TFLOP/s over visible pairs, tensor pipe 55% active), backward
+// 292 us (847 TFLOP/s over 5 products, 55 and 61% active over the 7 that run).
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -1534,7 +1534,7 @@ void take_attn(int64_t T, int64_t S, int32_t Hq, int32_t Hkv, int32_t Dh, Ws& ws
 
 // Small batches do without the planning kernel: where every unit has an SM of its own there is no
 // order to find, and with at most 32 samples a warp finds a unit's tile faster than a launch takes
-// (8 samples of up to 511 positions, 4 heads: about 3 us less a pass, 12 us forward and 20 us backward).
+// (8 samples of up to 511 positions, 4 heads: about 3 us less a pass, 12 us forward and 19 us backward).
 bool each_its_own(int64_t S, int64_t units) { return S <= 32 && units <= sm_count(); }
 
 // Allows a kernel its shared memory, once per device (`done` holds a bit for each).  A kernel
