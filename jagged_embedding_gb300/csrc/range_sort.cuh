@@ -16,7 +16,9 @@
 // themselves and drops those out of range.
 //
 // 2M IDs of 24 bits: 77 us for three passes; the library's sort for large tables, four
-// launches a pass over fixed tiles, takes 106 us here.
+// launches a pass over fixed tiles, takes 106 us here.  A row gradient call (rows of 32 bf16)
+// with this sort and that one: 20,000 IDs 63 and 91 us, 200,000 81 and 106, 2M 193 and 245,
+// 10M 735 and 794, 50M 3.69 and 3.51 ms: not worth a second way.
 #pragma once
 
 #include "fs_common.cuh"

@@ -11,7 +11,7 @@
 //      that crosses a tile's edge leaves partial sums;
 //   4. join: adds the partial sums of the rows that cross edges, in tile order
 //      (a hot row crosses thousands of tiles: a whole block adds those).
-// A small batch (at most 8192 entries) takes two launches instead of ten to sixteen: one block sorts and
+// A small batch (at most 8192 entries) takes two launches instead of seven to sixteen: one block sorts and
 // numbers in shared memory, then a warp sums each distinct row.
 // The order of every sum follows from the sorted order and T alone: results are
 // the same bits from run to run.
