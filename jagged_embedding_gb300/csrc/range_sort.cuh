@@ -125,8 +125,8 @@ static __global__ void __launch_bounds__(kScanThreads) scan_kernel(uint32_t* __r
 
 template <bool FIRST>
 __global__ void __launch_bounds__(kThreads, kPerSm) scatter_kernel(Entries in, int64_t T, int64_t* n_dev, int shift,
-                                                                   uint32_t mask, const uint32_t* __restrict__ counts,
-                                                                   const uint32_t* __restrict__ totals,
+                                                                   uint32_t mask, const uint32_t* counts,
+                                                                   const uint32_t* totals,
                                                                    uint32_t* __restrict__ out_k,
                                                                    uint32_t* __restrict__ out_v) {
   union Stage {

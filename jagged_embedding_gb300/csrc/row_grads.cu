@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_sort_kernel(const int6
                                                                       int kb, uint32_t* out_v, Numbering N,
                                                                       int32_t* err) {
   extern __shared__ uint32_t sm[];
-  asm volatile("griddepcontrol.launch_dependents;");
+  range_sort::launch_next();
   uint32_t* keys = sm;
   uint32_t* vals = keys + kSmallThreads * ITEMS;
   uint32_t* hist = vals + kSmallThreads * ITEMS;  // [warps][digits]
@@ -246,12 +246,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) small_sort_kernel(const int6
 // rows beside one another, kRedRows of them in flight per lane; their sums meet by
 // shuffles.  A row of more than kLongRow entries is taken by the block's eight warps.
 // blockIdx.y picks LPR * VEC columns of wider rows.
+// The blocks may be in place while the sort still writes vals, start and count: those are read
+// after the wait and past L1, and are not declared constant for this kernel's lifetime.
 constexpr int kSmallRowThreads = 256, kSmallRowWarps = kSmallRowThreads / 32, kLongRow = 48;
 
 template <class EI, class EO, int VEC, int LPR>
-__global__ void __launch_bounds__(kSmallRowThreads) grad_small_kernel(const uint32_t* __restrict__ vals,
-                                                                      const uint32_t* __restrict__ start,
-                                                                      const int64_t* __restrict__ count,
+__global__ void __launch_bounds__(kSmallRowThreads) grad_small_kernel(const uint32_t* vals, const uint32_t* start,
+                                                                      const int64_t* count,
                                                                       const void* __restrict__ dout, int32_t dim,
                                                                       float scale, void* __restrict__ grads, int64_t cap) {
   constexpr int SUB = 32 / LPR;
@@ -260,14 +261,14 @@ __global__ void __launch_bounds__(kSmallRowThreads) grad_small_kernel(const uint
   __shared__ float sums[kSmallRowWarps][LPR * VEC];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / LPR, c = (int(blockIdx.y) * LPR + lane % LPR) * VEC;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // (launched while the sort still runs)
-  const int64_t distinct = *count < cap ? *count : cap;
+  range_sort::wait_previous();
+  const int64_t found = __ldcg(count), distinct = found < cap ? found : cap;
   auto add = [&](float (&acc)[VEC], uint32_t e, uint32_t end, uint32_t step) {
     for (; e < end; e += 8 * step) {
       Raw<EI, VEC> g[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q)
-        if (e + q * step < end && c < dim) fetch<true>(g[q], dout, int64_t(__ldg(vals + e + q * step)) * dim + c);
+        if (e + q * step < end && c < dim) fetch<true>(g[q], dout, int64_t(__ldcg(vals + e + q * step)) * dim + c);
 #pragma unroll
       for (int q = 0; q < 8; ++q)
         if (e + q * step < end && c < dim) {
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(kSmallRowThreads) grad_small_kernel(const uint
   const int64_t u = int64_t(blockIdx.x) * kSmallRowWarps + warp;
   bool is_long = false;
   if (u < distinct) {
-    const uint32_t s = start[u], e = start[u + 1];
+    const uint32_t s = __ldcg(start + u), e = __ldcg(start + u + 1);
     is_long = e - s > uint32_t(kLongRow);
     if (!is_long) {
       float acc[VEC];
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(kSmallRowThreads) grad_small_kernel(const uint
     float acc[VEC];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
-    add(acc, start[ul] + warp * SUB + sub, start[ul + 1], SUB * kSmallRowWarps);
+    add(acc, __ldcg(start + ul) + warp * SUB + sub, __ldcg(start + ul + 1), SUB * kSmallRowWarps);
     if (sub == 0)
 #pragma unroll
       for (int k = 0; k < VEC; ++k) sums[warp][(lane % LPR) * VEC + k] = acc[k];
