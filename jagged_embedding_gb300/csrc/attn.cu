@@ -540,6 +540,20 @@ struct Place {
 __device__ __forceinline__ void wait_for_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;"); }
 
+// The block's tensor memory, and everyone's barriers and addresses in place; called by all
+// threads, `taker` one warp.  Only after wait_for_launch(): the launch before may still have to take tensor memory on
+// this SM, and a block that held all of it while waiting for that launch's end would never see it.  For the same
+// reason a kernel lets the next launch begin only after this.
+__device__ __forceinline__ void take_tmem(uint32_t* at, bool taker) {
+  if (taker) {
+    __syncwarp();
+    tc::alloc(at, 512);
+    tc::fence_before();
+  }
+  __syncthreads();
+  tc::fence_after();
+}
+
 // ------------------------------------------------------------- forward
 
 // A unit is two query tiles that read the same keys and values, so each loaded
@@ -621,15 +635,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
         bulk::mbar_init(bar + 8 * i, i == 1 ? 9 : (i == 4 || i == 5 ? 4 : 1));
       bulk::fence_init();
     }
-    __syncwarp();
-    tc::alloc(&tmem_at, 512);
-    tc::fence_before();
   } else if (warp == 9 && lane == 0) {
     tc::prefetch_map(&mq), tc::prefetch_map(&mk), tc::prefetch_map(&mv);
   }
-  __syncthreads();
-  tc::fence_after();
   wait_for_launch();
+  take_tmem(&tmem_at, warp == 8);
   const uint32_t s_at = tc::uni(tmem_at), o_at = s_at + 256;  // of query tile 0; tile 1's follow
 
   if (warp >= 8) {
@@ -901,15 +911,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
       for (int i = 0; i < 15 + 2 * NS; ++i) bulk::mbar_init(bar + 8 * i, i == 1 ? 9 : (i >= 5 && i <= 8 ? 8 : 1));
       bulk::fence_init();
     }
-    __syncwarp();
-    tc::alloc(&tmem_at, 512);
-    tc::fence_before();
   } else if (warp == 9 && lane == 0) {
     tc::prefetch_map(&mq), tc::prefetch_map(&mk), tc::prefetch_map(&mv), tc::prefetch_map(&mo), tc::prefetch_map(&mdo);
   }
-  __syncthreads();
-  tc::fence_after();
   wait_for_launch();
+  take_tmem(&tmem_at, warp == 8);
   let_next_launch();
   const uint32_t s_at = tc::uni(tmem_at), dq_at = s_at + 256;
   auto dp_at = [&](uint32_t tile) { return s_at + 128 + 256 * (tile & 1); };
@@ -1201,15 +1207,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
       for (int i = 0; i < 13 + 2 * NS; ++i) bulk::mbar_init(bar + 8 * i, i == 1 ? 9 : (i >= 4 && i <= 6 ? 8 : 1));
       bulk::fence_init();
     }
-    __syncwarp();
-    tc::alloc(&tmem_at, 512);
-    tc::fence_before();
   } else if (warp == 9 && lane == 0) {
     tc::prefetch_map(&mq), tc::prefetch_map(&mk), tc::prefetch_map(&mv), tc::prefetch_map(&mdo);
   }
-  __syncthreads();
-  tc::fence_after();
   wait_for_launch();
+  take_tmem(&tmem_at, warp == 8);
   const uint32_t s_at = tc::uni(tmem_at), dp_at = s_at + 128, dv_at = s_at + 256, dk_at = s_at + 256 + DH;
 
   if (warp == 9) {

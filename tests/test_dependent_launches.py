@@ -62,3 +62,14 @@ def test_no_read_only_loads_of_what_the_launch_before_writes(kernel):
     assert constant <= INPUTS, constant - INPUTS
     loads = {m.strip() for m in re.findall(r"__ldg\(\s*(?:reinterpret_cast<[^>]*>\s*\()?\s*([\w.\->]+)", body)}
     assert loads <= INPUT_LOADS, loads - INPUT_LOADS
+
+
+@pytest.mark.parametrize("kernel", [k for k in KERNELS if k[1].startswith("attn_")], ids=lambda k: k[1])
+def test_tensor_memory_is_taken_after_the_wait(kernel):
+    """Taken before it, a block could hold what the launch it waits for has yet to take, and neither would go on.
+    A kernel that lets the next launch begin has its own by then."""
+    body = kernel[3]
+    wait, take = body.index("wait_for_launch()"), [m.start() for m in re.finditer(r"take_tmem\(|tc::alloc\(", body)]
+    assert take and wait < min(take)
+    let = body.find("let_next_launch()")
+    assert let < 0 or max(take) < let
