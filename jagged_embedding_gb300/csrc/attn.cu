@@ -105,15 +105,16 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const int64_t* 
                                                                  int32_t* err) {
   __shared__ int32_t hist[2][kBuckets];
   __shared__ int32_t scan[32];
-  __shared__ unsigned long long work;
+  __shared__ unsigned long long work, listed;
   __shared__ int32_t nsplit;
   asm volatile("griddepcontrol.launch_dependents;");
   for (int i = threadIdx.x; i < 2 * kBuckets; i += kPlanThreads) (&hist[0][0])[i] = 0;
   if (threadIdx.x < 2) plan->next[threadIdx.x] = 0;
-  if (threadIdx.x == 0) work = 0, nsplit = 0;
+  if (threadIdx.x == 0) work = listed = 0, nsplit = 0;
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = span * kTile;
+  const int64_t most = T / kTile + (S < T ? S : T);  // entries the lists hold
   auto bucket = [](int cost) { return kBuckets - min(cost, kBuckets); };  // most work first
   // Query tiles that all key tiles of a sample meet.
   auto tiles_met = [&](int64_t L, int64_t uih) {
@@ -138,7 +139,10 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const int64_t* 
   // half of an SM's share, in query tiles of one unit's `group` heads
   const int64_t half = by_key ? int64_t(work) * kv_heads / (2 * sms) : 0;
   auto cut = [&](int nq) { return by_key && nq * group > 1 && nq > half; };
+  // f of every entry, as long as this warp's share fits the lists (it does where the offsets are in
+  // order); returns how many there are, in 64 bits: of samples that overlap there can be S * T / kTile.
   auto each = [&](bool report, auto f) {
+    int64_t entries = 0;
     for (int64_t s0 = int64_t(warp) * take; s0 < S; s0 += int64_t(kPlanWarps) * take) {
       int32_t begin = 0, L = 0, c = 0;
       if (lane < take && s0 + lane < S) {
@@ -163,6 +167,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const int64_t* 
         if (lane >= o) upto += y;
       }
       const int32_t all = __shfl_sync(0xffffffffu, upto, 31);
+      entries += all;
+      if (entries > most) continue;
       for (int32_t i0 = 0; i0 < all; i0 += 32) {
         const int32_t i = i0 + lane;
         int who = 0;  // lanes whose tiles end at or before i
@@ -183,26 +189,25 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const int64_t* 
         __syncwarp();
       }
     }
+    return entries;
   };
-  int64_t total = 0;
-  each(true, [&](const Tile&, int nk, int nq) {
+  const int64_t mine = each(true, [&](const Tile&, int nk, int nq) {
     atomicAdd(&hist[0][bucket(nk)], 1);
     if (by_key) atomicAdd(&hist[1][bucket(cut(nq) ? (nq + 1) / 2 : nq)], cut(nq) ? 2 : 1);
   });
+  if (lane == 0) atomicAdd(&listed, (unsigned long long)(mine));
   __syncthreads();
   for (int w = 0; w < (by_key ? 2 : 1); ++w) {
     int32_t n;
     const int32_t mine = hist[w][threadIdx.x];
     const int32_t at = block_exclusive_scan<int32_t>(mine, scan, &n);
     hist[w][threadIdx.x] = at;
-    if (w == 0) total = n;
     if (threadIdx.x == 0) plan->ntiles[w] = n;
   }
   __syncthreads();
   // Offsets that are not in order can describe more tiles than the lists hold:
   // then nothing is listed (the error word says so).
-  const int64_t most = T / kTile + (S < T ? S : T);
-  if (total > most) {
+  if (listed > (unsigned long long)(most)) {
     if (threadIdx.x == 0) {
       set_err(err, FS_ERR_BAD_OFFSETS);
       plan->ntiles[0] = plan->ntiles[1] = 0;
