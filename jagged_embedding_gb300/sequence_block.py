@@ -14,6 +14,7 @@ and back:
     rows, d table[rows]                             fs_emb_grad_rows
 
 The batch is one that `Pipeline.prepare` leaves (IDs sample by sample, [UIH | candidates]) or any other jagged one.
+Positions of no sample (before offsets[0], from offsets[-1] on, of a sample with bad offsets) attend to nothing: o = 0.
 The row gradients are for an optimizer of the caller's own; the fused update (fs_emb_update_sorted) takes d x directly.
 """
 from __future__ import annotations
@@ -62,7 +63,9 @@ class SequenceBlock:
         qkv = (y @ self.w_qkv).view(T, H + 2 * Hkv, Dh)
         q, k, v = qkv.split([H, Hkv, Hkv], dim=1)
         ws = self._workspace("attn", B.jagged_attn_workspace_size(T, offsets.numel() - 1, H, Hkv, Dh), ids.device)
-        o, lse, _ = B.fs_jagged_attn(q, k, v, offsets, self.scale, cand_len=cand_len, err=self.err, ws=ws)
+        # positions of no sample are left as they are by the call, and the products take every position
+        o = torch.zeros(T, H, Dh, dtype=torch.bfloat16, device=ids.device)
+        _, lse, _ = B.fs_jagged_attn(q, k, v, offsets, self.scale, cand_len=cand_len, out=o, err=self.err, ws=ws)
         z = o.view(T, H * Dh) @ self.w_out
         out, out_scale, h, rstd_out = B.fs_rmsnorm(z, self.gamma_out, self.eps, res=x,
                                                    y_dtype=torch.float8_e4m3fn if bits8 else None)
@@ -78,7 +81,7 @@ class SequenceBlock:
         dz, dgamma_out = B.fs_rmsnorm_backward(dout, h, self.gamma_out, rstd_out, dsum=dh, ws=norm_ws)
         do = (dz @ self.w_out.T).view(T, H, Dh)
         dw_out = o.view(T, H * Dh).T @ dz
-        dqkv = torch.empty_like(qkv)
+        dqkv = torch.zeros_like(qkv)  # (as o in the forward pass)
         q, k, v = qkv.split([H, Hkv, Hkv], dim=1)
         dq, dk, dv = dqkv.split([H, Hkv, Hkv], dim=1)
         ws = self._workspace("attn", B.jagged_attn_workspace_size(T, offsets.numel() - 1, H, Hkv, Dh), ids.device)

@@ -1,0 +1,67 @@
+"""The sequence block on batches that leave positions to no sample, and on several streams (GPU).
+
+Results are compared by the norm of the difference, at most 2^-6 of the norm: activations are bf16, and the worst
+of the products passes eight roundings of at most 2^-9 of the norm one after another.
+"""
+import pytest
+import torch
+
+from jagged_embedding_gb300.sequence_block import SequenceBlock
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16 = torch.bfloat16
+
+
+def _norm(x, w, eps):
+    return x * torch.rsqrt((x * x).mean(1, keepdim=True) + eps) * w
+
+
+def _reference(blk, table, ids, off, dout):
+    """The layer in 32 bits, the attention's output zero where a position is of no sample."""
+    p = {n: getattr(blk, n).float().requires_grad_() for n in ("w_qkv", "w_out", "gamma_in", "gamma_out")}
+    t = table.float().requires_grad_()
+    x = t[ids] * blk.emb_scale
+    T, H, Hkv, Dh = ids.numel(), blk.heads, blk.kv_heads, blk.head_dim
+    q, k, v = (_norm(x, p["gamma_in"], blk.eps) @ p["w_qkv"]).view(T, H + 2 * Hkv, Dh).split([H, Hkv, Hkv], dim=1)
+    k, v = k.repeat_interleave(H // Hkv, 1), v.repeat_interleave(H // Hkv, 1)
+    parts = [torch.zeros(off[0], H, Dh, device=DEV)]
+    for a, b in zip(off[:-1], off[1:]):
+        see = torch.ones(b - a, b - a, dtype=torch.bool, device=DEV).tril()
+        w = (torch.einsum("ihd,jhd->hij", q[a:b], k[a:b]) * blk.scale).masked_fill(~see, -float("inf"))
+        parts.append(torch.einsum("hij,jhd->ihd", torch.softmax(w, 2), v[a:b]))
+    parts.append(torch.zeros(T - off[-1], H, Dh, device=DEV))
+    out = _norm(x + torch.cat(parts).reshape(T, H * Dh) @ p["w_out"], p["gamma_out"], blk.eps)
+    (out * dout.float()).sum().backward()
+    return out.detach(), {"row_grads": t.grad, **{n: w.grad for n, w in p.items()}}
+
+
+def _poison(*shapes):
+    """Freed memory of these shapes, full of NaN: what an uninitialised tensor gets next."""
+    kept = [torch.full(s, float("nan"), dtype=BF16, device=DEV) for s in shapes for _ in range(4)]
+    torch.cuda.synchronize()
+    del kept
+
+
+def test_positions_of_no_sample():
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    R, D, T, H, Hkv = 700, 64, 1500, 2, 1
+    off = [100, 400, 400, 1130]
+    blk = SequenceBlock(D, H, Hkv, 64, generator=gen)
+    table = torch.randn(R, D, device=DEV, generator=gen)
+    ids = torch.randint(0, R, (T,), device=DEV, generator=gen)
+    dout = torch.randn(T, D, device=DEV, generator=gen).to(BF16)
+    want, grads = _reference(blk, table, ids, off, dout)
+    shapes = ((T, H, 64), (T, H + 2 * Hkv, 64), (T, (H + 2 * Hkv) * 64))
+    _poison(*shapes)
+    out, _, saved = blk.forward(table, ids, torch.tensor(off, device=DEV))
+    _poison(*shapes)
+    got = blk.backward(dout, saved)
+    blk.check()
+    rows = torch.unique(ids)
+    n = int(got["count"])
+    assert torch.equal(got["rows"][:n], rows)
+    got["row_grads"], grads["row_grads"] = got["row_grads"][:n], grads["row_grads"][rows]
+    for name, a, b in [("out", out, want)] + [(k, got[k], grads[k]) for k in grads]:
+        rel = float((a.double() - b.double()).norm() / b.double().norm())
+        assert rel < 2.0 ** -6, f"{name}: {rel}"
