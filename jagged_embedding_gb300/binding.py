@@ -150,6 +150,11 @@ def _stream(device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def current_stream(device):
+    """Handle of the stream that calls on tensors of `device` go to."""
+    return _stream(torch.device(device))
+
+
 def _need(t, dtype, name, numel=None):
     if t.device.type != "cuda":
         raise FsError(1, f"{name} must be a CUDA tensor")

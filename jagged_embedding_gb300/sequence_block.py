@@ -48,10 +48,12 @@ class SequenceBlock:
         self._ws = {}
 
     def _workspace(self, name, nbytes, device):
-        """Workspaces are kept and grow with the batch."""
-        ws = self._ws.get(name)
+        """Workspaces are kept and grow with the batch, each for the current stream alone: calls on several streams
+        may run at once, and what a stream outgrows is freed in that stream's order."""
+        key = name, device, B.current_stream(device)
+        ws = self._ws.get(key)
         if ws is None or ws.numel() < nbytes:
-            ws = self._ws[name] = B.workspace(nbytes, device)
+            ws = self._ws[key] = B.workspace(nbytes, device)
         return ws
 
     def forward(self, table, ids, offsets, cand_len=None, bits8=False):
