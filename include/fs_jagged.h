@@ -502,7 +502,7 @@ fs_status fs_emb_grad_rows(int64_t num_rows, int32_t dim, const int64_t* ids, in
  *   x, res, sum_out [T, dim] of dtype (FS_F32 or FS_BF16); res and sum_out both or
  *   neither; sum_out may be x or res (in place).  gamma [dim] fp32.  y [T, dim] of y_dtype;
  *   y_scale [T] fp32, for FS_E4M3 only (NULL otherwise); rstd [T] fp32 = r, or NULL.
- * 1 <= dim <= 8192, eps >= 0.
+ * 1 <= dim <= 8192, eps >= 0.  With T = 0 nothing is done and any row pointer may be NULL.
  *
  * fs_rmsnorm_backward: with n_d = h_d * r and w_d = gamma_d * dy_d
  *   dh_d = dsum_d + r * (w_d - n_d * mean_e(w_e * n_e))   the gradient of x and of res

@@ -379,8 +379,9 @@ extern "C" fs_status fs_rmsnorm(const void* x, const void* res, int64_t T, int32
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (T < 0 || T > INT32_MAX || dim < 1 || dim > kMaxNormDim || !(eps >= 0.f)) return FS_ERR_INVALID_ARG;
   if ((dtype != FS_F32 && dtype != FS_BF16) || (y_dtype != dtype && y_dtype != FS_E4M3)) return FS_ERR_INVALID_ARG;
+  if (y_dtype != FS_E4M3 && y_scale) return FS_ERR_INVALID_ARG;
+  if (T == 0) return FS_OK;  // (an empty tensor's pointer may be NULL)
   if ((res == nullptr) != (sum_out == nullptr) || (y_dtype == FS_E4M3) != (y_scale != nullptr)) return FS_ERR_INVALID_ARG;
-  if (T == 0) return FS_OK;
   if (!x || !gamma || !y) return FS_ERR_INVALID_ARG;
   const size_t eb = dtype == FS_F32 ? 4 : 2, yb = y_dtype == FS_E4M3 ? 1 : eb;
   if (!aligned(x, eb) || !aligned(res, eb) || !aligned(sum_out, eb) || !aligned(y, yb) || !aligned(gamma, 4) ||
