@@ -89,7 +89,7 @@ class SequenceBlock:
         ws = self._workspace("attn", B.jagged_attn_workspace_size(T, offsets.numel() - 1, H, Hkv, Dh), ids.device)
         B.fs_jagged_attn_backward(q, k, v, o, lse, do, offsets, self.scale, cand_len=cand_len, dq=dq, dk=dk, dv=dv,
                                   err=self.err, ws=ws)
-        flat = dqkv.view(T, -1)
+        flat = dqkv.view(T, (H + 2 * Hkv) * Dh)
         dx, dgamma_in = B.fs_rmsnorm_backward(flat @ self.w_qkv.T, x, self.gamma_in, rstd, dsum=dz, ws=norm_ws)
         grad_ws = self._workspace("rows", B.emb_grad_rows_workspace_size(T, num_rows, self.dim), ids.device)
         rows, row_grads, count, _ = B.fs_emb_grad_rows(ids, dx, num_rows, self.emb_scale, grad_dtype=grad_dtype,

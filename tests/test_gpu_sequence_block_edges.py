@@ -104,3 +104,19 @@ def test_two_streams_at_once():
                 assert float((r[name].double() - w[name].double()).norm()) <= 2.0 ** -6 * float(w[name].double().norm()), name
             a, b = r["row_grads"][:n].double(), w["row_grads"][:n].double()
             assert float((a - b).norm()) <= 2.0 ** -6 * float(b.norm())
+
+
+@pytest.mark.parametrize("samples", [0, 3])
+def test_batch_without_positions(samples):
+    R, D = 50, 64
+    blk = SequenceBlock(D, 2, 1, 64)
+    table = torch.randn(R, D, device=DEV)
+    ids = torch.empty(0, dtype=torch.int64, device=DEV)
+    for bits8 in (False, True):
+        out, scale, saved = blk.forward(table, ids, torch.zeros(samples + 1, dtype=torch.int64, device=DEV), bits8=bits8)
+        assert out.shape == (0, D) and (scale is None or scale.shape == (0,))
+        got = blk.backward(torch.empty(0, D, dtype=BF16, device=DEV), saved)
+        blk.check()
+        assert int(got["count"]) == 0
+        for name in ("w_qkv", "w_out", "gamma_in", "gamma_out"):
+            assert got[name].shape == getattr(blk, name).shape and not got[name].any()
