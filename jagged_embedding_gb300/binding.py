@@ -722,7 +722,7 @@ def _rows(t, T, heads, dim, name, device):
     s = t.stride()
     if (dim > 1 and s[2] != 1) or (heads > 1 and s[1] != dim):
         raise FsError(1, f"{name}: the heads of a position must be contiguous")
-    return s[0] if T > 1 else max(s[0], heads * dim)
+    return s[0] if T > 1 else heads * dim  # (a single row has no stride of its own)
 
 
 def jagged_attn_workspace_size(T, S, heads, kv_heads, head_dim):
