@@ -496,8 +496,8 @@ fs_status fs_emb_grad_rows(int64_t num_rows, int32_t dim, const int64_t* ids, in
  *   h = x + res, stored in dtype (sum_out); h = x when res is NULL
  *   r = 1 / sqrt(mean_d(h_d^2) + eps);   y_d = h_d * r * gamma_d
  *   y_dtype = dtype: y rounded once.  y_dtype = FS_E4M3: y_scale = max_d |y_d| / 448
- *   and y = e4m3(y_d / y_scale), to nearest even; a row of zeros has scale 0
- *   and zeros.  A row with a NaN or an infinity has a NaN scale (or NaN values).
+ *   and y = e4m3 of the fp32 quotient y_d / y_scale, to nearest even; a row of zeros has
+ *   scale 0 and zeros.  A row with a NaN or an infinity has a NaN scale (or NaN values).
  * The norm is of h as stored, so the backward pass differentiates what was computed.
  *   x, res, sum_out [T, dim] of dtype (FS_F32 or FS_BF16); res and sum_out both or
  *   neither; sum_out may be x or res (in place).  gamma [dim] fp32.  y [T, dim] of y_dtype;
