@@ -46,3 +46,20 @@ def test_batches_in_turn_over_one_workspace():
         n = uniq.numel()
         assert int(count) == n and torch.equal(rows[:n], uniq), k
         assert torch.equal(grads[:n].double().cpu(), ref), k
+
+
+@pytest.mark.parametrize("R", [10_000_000, 1 << 31, (1 << 32) - 1])
+@pytest.mark.parametrize("T", [1024, 1025, 2048, 3073, 4096, 4097, 6144, 6145, 8192])
+def test_every_block_shape_and_number_of_passes(T, R):
+    """One to eight entries a thread, three and four passes; IDs out of range sort behind the last row."""
+    ids, dout = _batch(T, R, 32, T)
+    for bad in (False, True):
+        if bad:
+            ids = ids.clone()
+            ids[1], ids[T // 3], ids[T - 1] = -1, R, 1 << 40
+        rows, grads, count, err = B.fs_emb_grad_rows(ids, dout, R, 2.0)
+        assert int(err) == (2 if bad else 0)
+        uniq, ref = _expect(ids, dout, R)
+        n = uniq.numel()
+        assert int(count) == n and torch.equal(rows[:n], uniq)
+        assert torch.equal(grads[:n].double().cpu(), ref * 2)
