@@ -662,6 +662,7 @@ extern "C" fs_status fs_emb_grad_rows(int64_t num_rows, int32_t dim, const int64
   const size_t ib = dout_dtype == FS_F32 ? 4 : 2, ob = grad_dtype == FS_F32 ? 4 : 2;
   if (!aligned(ids, 8) || !aligned(rows, 8) || !aligned(dout, ib) || !aligned(row_grads, ob)) return FS_ERR_ALIGNMENT;
   if (!ws || ws_bytes < fs_emb_grad_rows_workspace_size(T, num_rows, dim)) return FS_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return FS_ERR_ALIGNMENT;  // (sorted entries and partial sums move in 16-byte accesses)
 
   const GradLayout L = grad_layout(T);
   WsCursor cur(ws, ws_bytes);
