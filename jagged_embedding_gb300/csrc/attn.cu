@@ -98,7 +98,7 @@ constexpr int64_t most_split(int64_t sms) { return 2 * sms; }
 // A key tile whose units (one per key/value head, over `group` query heads) each take more than half of
 // an SM's share of the whole work is listed as two halves: in a batch with a few long samples
 // one such unit would otherwise set the time.
-__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const int64_t* __restrict__ offsets, int64_t S, int64_t T,
+__global__ void __launch_bounds__(kPlanThreads, 1) attn_plan_kernel(const int64_t* __restrict__ offsets, int64_t S, int64_t T,
                                                                  const int32_t* __restrict__ cand, bool causal,
                                                                  int span, int kv_heads, int group, int sms, Plan* plan,
                                                                  Tile* by_query, Tile* by_key, int32_t* flags,
