@@ -533,7 +533,8 @@ fs_status fs_rmsnorm_backward(const void* dy, const void* dsum, const void* h, i
  *   dq_i = scale * sum_j ds_ij k_j;  dk_j = scale * sum_i ds_ij q_i;  dv_j = sum_i p_ij dout_i
  * Query head h reads key/value head h * kv_heads / heads; dk and dv sum over the
  * query heads that share it.  All rows are bf16; products accumulate in fp32, the
- * softmax is fp32; p and ds enter their products rounded to bf16.
+ * softmax is fp32; p and ds enter their products rounded to bf16 (in the backward pass of a small
+ * batch, up to 32 samples and a tile and head per SM, as pairs of bf16: 2^-17).
  *   q [T, heads, head_dim], k, v [T, kv_heads, head_dim]: rows *_stride elements apart
  *     (slices of one projection's output), 16-byte aligned, strides multiples of 8;
  *     dq, dk, dv likewise.  out, dout [T, heads, head_dim] contiguous.  lse [heads, T] fp32.

@@ -26,6 +26,15 @@
 // has a fixed order and nothing is added atomically; it recomputes x and do.v
 // twice (7 products where a pass with atomic sums of dq needs 5).
 //
+// Scores, softmax statistics, sums and accumulators are fp32.  p and ds are rounded to bf16, since the tensor cores
+// take both operands in the type of q, k and v: each error is 2^-9 of its own term and they are as many as the
+// terms, so a result is off by about as much again as by its own rounding to bf16 (relative norms against 64 bits:
+// out 2.0e-3, gradients 2.4e-3, where rounding alone leaves 1.7e-3).  A backward pass over a small batch, in which
+// each unit has an SM of its own, takes p and ds as pairs of bf16 (FINE: 2^-17, a second product for the rests, in the
+// half of the columns that the rounded values leave free): with few terms the errors may come together
+// by chance (1 batch in 250 had half as much again), and the products are not what such a batch waits for.  8 samples of up
+// to 511 positions: gradients 2.4e-3 -> 1.7e-3, 19.1 -> 21.7 us; 22,000 positions of long histories would pay 323 -> 423 us.
+//
 // Bound on long samples by the tensor cores and the hand-overs between products
 // and elementwise warps, on short ones by the chain of latencies inside one unit.
 // 22,000 positions of causal samples up to 4096, 8 query and 2 key/value heads of 128:
@@ -35,6 +44,7 @@
 
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 #include <utility>
 
 #include "fs_common.cuh"
@@ -523,6 +533,12 @@ __device__ __forceinline__ void store32(__nv_bfloat16* to, int64_t stride, int l
       *reinterpret_cast<uint4*>(to + int64_t(4 * q + j) * stride + 8 * s) = make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
 }
 
+// What two fp32 values leave when they are rounded to the bf16 pair `w`, itself as a bf16 pair: together within
+// 2^-17 of the values.
+__device__ __forceinline__ uint32_t rest2(uint32_t w, float lo, float hi) {
+  return tc::pack2(lo - __uint_as_float(w << 16), hi - __uint_as_float(w & 0xFFFF0000u));
+}
+
 template <int DH>
 constexpr int tile_bytes() { return DH / 64 * kBox; }
 
@@ -893,7 +909,7 @@ struct DqUnit {
   }
 };
 
-template <int DH>
+template <int DH, bool FINE>
 __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_constant__ CUtensorMap mq,
                                                                  const __grid_constant__ CUtensorMap mk,
                                                                  const __grid_constant__ CUtensorMap mv,
@@ -991,6 +1007,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
       if (!wait(ds_ready + 8 * (sums & 1), sums >> 1, a)) return false;
       tc::fence_after();
       mma_cols<DH>(dq_at, dp, dp + 64, kq_desc, acc);
+      if (FINE) mma_cols<DH>(dq_at, dp + 32, dp + 96, kq_desc, true);
       tc::commit(k_free);
       if (last) tc::commit(dq_full);
       kq.skip(2);
@@ -1107,7 +1124,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
           }
           if (!(ok = join_delta(d, delta))) break;
         }
-        uint32_t w[32];
+        uint32_t w[32], rest[32];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           float g[32];
@@ -1124,9 +1141,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
             for (int i = 0; i < 32; ++i) g[i] = (32 * b + i < lim || 32 * b + i == self) ? g[i] : 0.f;
           }
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) w[16 * b + i / 2] = tc::pack2(g[i], g[i + 1]);
+          for (int i = 0; i < 32; i += 2) {
+            w[16 * b + i / 2] = tc::pack2(g[i], g[i + 1]);
+            if (FINE) rest[16 * b + i / 2] = rest2(w[16 * b + i / 2], g[i], g[i + 1]);
+          }
         }
         tc::st32(dp, w);
+        if (FINE) tc::st32(dp + 32, rest);
         tc::wait_st();
         tc::fence_before();
         __syncwarp();
@@ -1190,7 +1211,7 @@ struct QueryWalk {
   }
 };
 
-template <int DH>
+template <int DH, bool FINE>
 __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_constant__ CUtensorMap mq,
                                                                   const __grid_constant__ CUtensorMap mk,
                                                                   const __grid_constant__ CUtensorMap mv,
@@ -1277,6 +1298,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
           tc::fence_after();
           if (sum) {
             mma_cols<DH>(dv_at, s_at, s_at + 64, do_desc, j != 0);
+            if (FINE) mma_cols<DH>(dv_at, s_at + 32, s_at + 96, do_desc, true);
             tc::commit(do_free);
           }
           if (more) {
@@ -1291,6 +1313,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
         tc::fence_after();
         if (sum) {
           mma_cols<DH>(dk_at, dp_at, dp_at + 64, q_desc, j != 0);
+          if (FINE) mma_cols<DH>(dk_at, dp_at + 32, dp_at + 96, q_desc, true);
           tc::commit(q_free);
         }
         if (more) {
@@ -1367,10 +1390,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
 #pragma unroll
           for (int i = 0; i < 64; ++i) p[i] = (i >= from || i == self) ? p[i] : 0.f;
         }
-        uint32_t pk[32];
+        uint32_t pk[32], rest[32];
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) pk[i / 2] = tc::pack2(p[i], p[i + 1]);
+        for (int i = 0; i < 64; i += 2) {
+          pk[i / 2] = tc::pack2(p[i], p[i + 1]);
+          if (FINE) rest[i / 2] = rest2(pk[i / 2], p[i], p[i + 1]);
+        }
         tc::st32(s_at + lanes + cols, pk);
+        if (FINE) tc::st32(s_at + lanes + cols + 32, rest);
         tc::wait_st();
         tc::fence_before();
         __syncwarp();
@@ -1393,9 +1420,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
             tc::mul2(g + i + 2, p[32 * b + i + 2], p[32 * b + i + 3]);
             pk[16 * b + i / 2] = tc::pack2(g[i], g[i + 1]);
             pk[16 * b + i / 2 + 1] = tc::pack2(g[i + 2], g[i + 3]);
+            if (FINE) {
+              rest[16 * b + i / 2] = rest2(pk[16 * b + i / 2], g[i], g[i + 1]);
+              rest[16 * b + i / 2 + 1] = rest2(pk[16 * b + i / 2 + 1], g[i + 2], g[i + 3]);
+            }
           }
         }
         tc::st32(dp_at + lanes + cols, pk);
+        if (FINE) tc::st32(dp_at + lanes + cols + 32, rest);
         tc::wait_st();
         tc::fence_before();
         __syncwarp();
@@ -1577,7 +1609,7 @@ void launch_after(void (*kern)(Params...), int64_t grid, int threads, int smem, 
   cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
-std::atomic<uint64_t> g_fwd_ready[2], g_bwd_ready[2][2];
+std::atomic<uint64_t> g_fwd_ready[2];
 
 }  // namespace
 }  // namespace fs
@@ -1691,17 +1723,23 @@ extern "C" fs_status fs_jagged_attn_backward(const void* q, int64_t q_stride, co
   const int64_t gq = tiles * heads < sms ? tiles * heads : sms, gk = 2 * tiles * kv_heads < sms ? 2 * tiles * kv_heads : sms;
   AttnArgs b = a;
   a.tiles = W.by_query, b.tiles = W.by_key;
-  if (head_dim == 64) {
-    if (!prepare_kernel(attn_dq_kernel<64>, bwd_smem<64>(), 0, g_bwd_ready[0][0])) return FS_ERR_CUDA;
-    if (!prepare_kernel(attn_dkv_kernel<64>, bwd_smem<64>(), 0, g_bwd_ready[0][1])) return FS_ERR_CUDA;
-    launch_after(attn_dq_kernel<64>, gq, kBwdThreads, bwd_smem<64>(), st, mq, mk, mv, mo, mdo, a);
-    launch_after(attn_dkv_kernel<64>, gk, kBwdThreads, bwd_smem<64>(), st, mq, mk, mv, mdo, b);
-  } else {
-    if (!prepare_kernel(attn_dq_kernel<128>, bwd_smem<128>(), 0, g_bwd_ready[1][0])) return FS_ERR_CUDA;
-    if (!prepare_kernel(attn_dkv_kernel<128>, bwd_smem<128>(), 0, g_bwd_ready[1][1])) return FS_ERR_CUDA;
-    launch_after(attn_dq_kernel<128>, gq, kBwdThreads, bwd_smem<128>(), st, mq, mk, mv, mo, mdo, a);
-    launch_after(attn_dkv_kernel<128>, gk, kBwdThreads, bwd_smem<128>(), st, mq, mk, mv, mdo, b);
-  }
+  auto launch = [&](auto dh, auto fine) {
+    constexpr int DH = decltype(dh)::value;
+    constexpr bool FINE = decltype(fine)::value;
+    static std::atomic<uint64_t> ready[2];
+    if (!prepare_kernel(attn_dq_kernel<DH, FINE>, bwd_smem<DH>(), 0, ready[0]) ||
+        !prepare_kernel(attn_dkv_kernel<DH, FINE>, bwd_smem<DH>(), 0, ready[1]))
+      return false;
+    launch_after(attn_dq_kernel<DH, FINE>, gq, kBwdThreads, bwd_smem<DH>(), st, mq, mk, mv, mo, mdo, a);
+    launch_after(attn_dkv_kernel<DH, FINE>, gk, kBwdThreads, bwd_smem<DH>(), st, mq, mk, mv, mdo, b);
+    return true;
+  };
+  using std::integral_constant;
+  const integral_constant<int, 64> d64;
+  const integral_constant<int, 128> d128;
+  const bool ok = !listed ? (head_dim == 64 ? launch(d64, std::true_type{}) : launch(d128, std::true_type{}))
+                          : (head_dim == 64 ? launch(d64, std::false_type{}) : launch(d128, std::false_type{}));
+  if (!ok) return FS_ERR_CUDA;
   count_launch(listed ? 3 : 2);
   return launch_status();
 }
