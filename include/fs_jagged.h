@@ -543,8 +543,10 @@ fs_status fs_rmsnorm_backward(const void* dy, const void* dsum, const void* h, i
  *     FS_ERR_BAD_OFFSETS and the sample is skipped.
  *   cand_len [S] int32 in [0, L], or NULL (no candidates); outside sets
  *     FS_ERR_INVALID_ARG and is clamped.
- * Samples never mix (a NaN in one does not reach another); inside a sample a NaN or an
- * infinity in k or v may reach rows that do not see it.
+ * Samples never mix (a NaN in one does not reach another).  Inside a sample a NaN or an infinity may
+ * reach rows that do not see it: one in v the outputs of rows in the same tiles of 128, one in q, k, v
+ * or dout their gradients.  A candidate is one position: several IDs of one candidate cannot see one
+ * another.  No output overlaps an input.
  * head_dim 64 or 128; heads a multiple of kv_heads; scale > 0.  Sums have a fixed
  * order: the same bits run to run.  The workspace (the same query for both passes) holds nothing between calls.
  * ---------------------------------------------------------------------- */

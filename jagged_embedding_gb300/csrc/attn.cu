@@ -38,8 +38,9 @@
 // Bound on long samples by the tensor cores and the hand-overs between products
 // and elementwise warps, on short ones by the chain of latencies inside one unit.
 // 22,000 positions of causal samples up to 4096, 8 query and 2 key/value heads of 128:
-// forward 91 us (1090 TFLOP/s over visible pairs, tensor pipe 55% active), backward
-// 292 us (847 TFLOP/s over 5 products, 55 and 61% active over the 7 that run).
+// forward 93 us (1070 TFLOP/s over visible pairs, tensor pipe 55% active), backward
+// 291 us (850 TFLOP/s over 5 products, 55 and 61% active over the 7 that run).  350,000 positions in 256 such
+// samples: 1.7 ms (1210 TFLOP/s) and 5.7 ms (900); with heads of 64 1.1 ms (920) and 3.7 ms (690).
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -888,7 +889,8 @@ __device__ __forceinline__ Tile uniform_tile(Tile x) {
 // delta = dout.out: the unit's rows of out come through the ring in front of its
 // keys.  Where there is one key tile delta = sum p * (do v^T) is at hand instead, free of the rounding
 // of out, which matters most there: few keys leave out about as large as v (8 samples of up to
-// 511 positions: dq and dk 2.6e-3 from 64 bits with dout.out, 2.4e-3 with the sum; bf16 results alone are 1.7e-3).
+// 511 positions, p and ds rounded once: dq and dk 2.6e-3 from 64 bits with dout.out, 2.4e-3 with the sum;
+// bf16 results alone are 1.7e-3).
 struct DqUnit {
   Tile x;
   int head, kv_head, nk, n;  // n < 0: no more units
@@ -1573,7 +1575,7 @@ void take_attn(int64_t T, int64_t S, int32_t Hq, int32_t Hkv, int32_t Dh, Ws& ws
 
 // Small batches do without the planning kernel: where every unit has an SM of its own there is no
 // order to find, and with at most 32 samples a warp finds a unit's tile faster than a launch takes
-// (8 samples of up to 511 positions, 4 heads: about 3 us less a pass, 12 us forward and 19 us backward).
+// (8 samples of up to 511 positions, 4 heads: about 3 us less a pass, 12 to 14 us forward and 21 to 22 backward).
 bool each_its_own(int64_t S, int64_t units) { return S <= 32 && units <= sm_count(); }
 
 // Allows a kernel its shared memory, once per device (`done` holds a bit for each).  A kernel

@@ -26,9 +26,9 @@
 namespace fs {
 namespace range_sort {
 
-// Block shape: 256 x 16 entries in 64 registers, 4 blocks per SM, so that 2M entries are one tile a
-// block (a row gradient call 252 us; 512 x 8 in 32 registers 262, 1024 x 7 265, 5 blocks per SM 271,
-// 3 264; match.any in place of the ballots 261).
+// Block shape: 256 x 16 entries in 64 registers, 4 blocks per SM: the entries in registers of all
+// blocks together are 2.5M, and fewer, larger tiles mean fewer barriers (a row gradient call of 2M entries 252 us;
+// 512 x 8 in 32 registers 262, 1024 x 7 265, 5 blocks per SM 271, 3 264; match.any in place of the ballots 261).
 constexpr int kThreads = 256, kWarps = kThreads / 32, kItems = 16, kTile = kThreads * kItems;
 constexpr int kBits = 8, kBins = 1 << kBits;
 constexpr int kPerSm = 4;            // resident blocks per SM

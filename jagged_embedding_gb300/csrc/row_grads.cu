@@ -20,7 +20,7 @@
 // distinct ID; the sort moves about 20 B per ID and pass beside that.  2M Zipf IDs
 // over 10M rows, bf16 rows of 128 into fp32 rows: 252 us a call -- sort 77, numbering
 // 19, reduce 138 (0.79 GB, 5.7 TB/s), join 14 -- of which those bytes alone would take 124.
-// 2000 IDs: 17 us, half of it the one block that sorts.
+// 2000 IDs: 18 us, half of it the one block that sorts.
 #include <atomic>
 
 #include "convert.cuh"
